@@ -62,6 +62,45 @@ class Params(ctypes.Structure):
     ]
 
 
+FP_SCALE_NONE, FP_SCALE_HEAD, FP_SCALE_TOKEN = 0, 1, 2
+
+
+class CacheParams(ctypes.Structure):
+    """Mirror of ``fp_cache_t``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("scale", ctypes.c_int),
+        ("batch", ctypes.c_int),
+        ("hkv", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("num_pages", ctypes.c_int),
+        ("max_pages_per_req", ctypes.c_int),
+        ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+    ]
+
+
+class TreeParams(ctypes.Structure):
+    """Mirror of ``fp_tree_t``."""
+
+    _fields_ = [
+        ("hq", ctypes.c_int),
+        ("total_tokens", ctypes.c_int),
+        ("max_tokens", ctypes.c_int),
+        ("softmax_scale", ctypes.c_float),
+        ("q_stride", ctypes.c_longlong),
+        ("cu_tokens", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p),
+        ("mask_words", ctypes.c_int),
+    ]
+
+
 _lib = None
 
 
@@ -72,7 +111,8 @@ def load_library(path: str) -> ctypes.CDLL:
         raise RuntimeError(f"{path} is missing: build it with `python -m block_sparse_long_blocks_b200.build`")
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(Params)
-    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    CP, TP = ctypes.POINTER(CacheParams), ctypes.POINTER(TreeParams)
+    vp, sz, ll = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_longlong
     sig = {
         "fp_workspace_size": (sz, [P]),
         "fp_mask_words": (sz, [P]),
@@ -89,6 +129,11 @@ def load_library(path: str) -> ctypes.CDLL:
         "fp_discover_compact_static": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp]),
         "fp_prefill": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "fp_static_scratch_bytes": (sz, []),
+        "fp_cache_write": (ctypes.c_int, [CP, vp, ctypes.c_int, vp, ll, vp, ll, vp]),
+        "fp_cache_read": (ctypes.c_int, [CP, vp, ctypes.c_int, vp, vp, ll, vp, ll, vp]),
+        "fp_cache_commit": (ctypes.c_int, [CP, vp, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp]),
+        "fp_tree_workspace_size": (sz, [CP, TP]),
+        "fp_tree_attention": (ctypes.c_int, [CP, TP, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -271,6 +316,162 @@ def fp_get_device_status(stream=None) -> int:
     if code not in (0, -6):
         raise FPError("fp_get_device_status", code)
     return int(bits.value)
+
+
+# ----------------------------------------------------------------------------
+# the paged cache and the decoding steps over it
+# ----------------------------------------------------------------------------
+
+def _expect(fn: str, what: str, ok: bool):
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+def _int32(fn: str, name: str, t: torch.Tensor, device, shape=None):
+    _expect(fn, f"{name} must be a contiguous int32 tensor on {device}"
+            + ("" if shape is None else f" of shape {tuple(shape)}"),
+            t.dtype is torch.int32 and t.device == device and t.is_contiguous()
+            and (shape is None or tuple(t.shape) == tuple(shape)))
+
+
+class Cache:
+    """A paged KV cache (``fp_cache_t``): pools [pages, page, hkv, d], bf16 or
+    float8_e4m3fn; page_table int32 [batch, max_pages]; kv_lens int32 [batch]
+    (cached tokens of every request, the new tokens of the call included; read
+    on the device, so a program updates it in place). e4m3 pools take float32
+    scales: [hkv] (one per KV head) or [pages, hkv, page] (one per token and
+    head, written by ``fp_cache_write``). Holds the tensors; copies nothing."""
+
+    def __init__(self, k_pool, v_pool, page_table, kv_lens, k_scale=None, v_scale=None):
+        fn = "Cache"
+        _expect(fn, "pools must be 4-D [pages, page, hkv, d], contiguous, of one shape, type and device",
+                k_pool.dim() == 4 and k_pool.shape == v_pool.shape and k_pool.dtype == v_pool.dtype
+                and k_pool.device == v_pool.device and k_pool.is_contiguous() and v_pool.is_contiguous())
+        _expect(fn, "pools must be bfloat16 or float8_e4m3fn",
+                k_pool.dtype in (torch.bfloat16, torch.float8_e4m3fn))
+        pages, page, hkv, d = k_pool.shape
+        _expect(fn, "page_table must be 2-D", page_table.dim() == 2)
+        _int32(fn, "page_table", page_table, k_pool.device)
+        _int32(fn, "kv_lens", kv_lens, k_pool.device, (page_table.shape[0],))
+        scale = FP_SCALE_NONE
+        if k_pool.dtype is torch.float8_e4m3fn:
+            _expect(fn, "e4m3 pools need k_scale and v_scale", k_scale is not None and v_scale is not None)
+            scale = FP_SCALE_TOKEN if k_scale.dim() == 3 else FP_SCALE_HEAD
+            shape = (pages, hkv, page) if scale == FP_SCALE_TOKEN else (hkv,)
+            for s in (k_scale, v_scale):
+                _expect(fn, f"scales must be contiguous float32 [hkv] or [pages, hkv, page], here {shape}",
+                        tuple(s.shape) == shape and s.dtype is torch.float32 and s.device == k_pool.device
+                        and s.is_contiguous())
+        else:
+            _expect(fn, "bf16 pools take no scales", k_scale is None and v_scale is None)
+        self.tensors = (k_pool, v_pool, page_table, kv_lens, k_scale, v_scale)
+        self.device, self.hkv, self.head_dim, self.batch = k_pool.device, hkv, d, page_table.shape[0]
+        self.p = CacheParams(
+            dtype=FP_BF16 if scale == FP_SCALE_NONE else FP_E4M3, scale=scale, batch=self.batch, hkv=hkv, head_dim=d,
+            page_size=page, num_pages=pages, max_pages_per_req=page_table.shape[1], k_pool=k_pool.data_ptr(),
+            v_pool=v_pool.data_ptr(), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale), page_table=page_table.data_ptr(),
+            kv_lens=kv_lens.data_ptr())
+        self.ref = ctypes.byref(self.p)
+
+
+def _launch_stream(fn: str, device, stream) -> int:
+    """The stream of a call whose tensors live on `device`: launches go to the
+    current device, so the two have to agree."""
+    _expect(fn, f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}",
+            device.index == torch.cuda.current_device())
+    return _stream(stream)
+
+
+def _rows(fn: str, cache: Cache, cu, k, v):
+    _int32(fn, "cu_tokens", cu, cache.device, (cache.batch + 1,))
+    for x in (k, v):
+        _expect(fn, f"k and v must be bfloat16 [tokens, {cache.hkv}, {cache.head_dim}] on {cache.device}, "
+                "contiguous within a token",
+                x.dtype is torch.bfloat16 and x.dim() == 3 and x.shape[1] == cache.hkv
+                and x.shape[2] == cache.head_dim and x.shape[0] == k.shape[0] and x.device == cache.device
+                and x.stride(2) == 1 and (x.stride(1) == cache.head_dim or cache.hkv == 1))
+    total = k.shape[0]
+    row = cache.hkv * cache.head_dim
+    # (the stride of a single row is whatever its tensor happens to say)
+    return total, *(x.stride(0) if total > 1 else row for x in (k, v))
+
+
+def fp_cache_write(cache: Cache, cu_tokens, k, v, stream=None):
+    """Writes new tokens' K and V (bf16 [tokens, hkv, d], any token stride) into the cache."""
+    total, ks, vs = _rows("fp_cache_write", cache, cu_tokens, k, v)
+    s = _launch_stream("fp_cache_write", cache.device, stream)
+    _check("fp_cache_write", load().fp_cache_write(cache.ref, cu_tokens.data_ptr(), total, k.data_ptr(), ks,
+                                                   v.data_ptr(), vs, s))
+
+
+def fp_cache_read(cache: Cache, cu_tokens, k, v, starts=None, stream=None):
+    """Reads cached tokens into k and v (bf16 [tokens, hkv, d]): the last ones of
+    every request, or those from ``starts`` on."""
+    total, ks, vs = _rows("fp_cache_read", cache, cu_tokens, k, v)
+    if starts is not None:
+        _int32("fp_cache_read", "starts", starts, cache.device, (cache.batch,))
+    s = _launch_stream("fp_cache_read", cache.device, stream)
+    _check("fp_cache_read", load().fp_cache_read(cache.ref, cu_tokens.data_ptr(), total, _ptr(starts), k.data_ptr(),
+                                                 ks, v.data_ptr(), vs, s))
+
+
+def fp_cache_commit(cache: Cache, cu_tokens, total_tokens: int, accept, num_accept, new_lens, stream=None):
+    """Moves the accepted new tokens' rows to the positions they keep and writes
+    the requests' new lengths (``new_lens`` may be the cache's kv_lens)."""
+    fn = "fp_cache_commit"
+    _int32(fn, "cu_tokens", cu_tokens, cache.device, (cache.batch + 1,))
+    _expect(fn, f"accept must be [{cache.batch}, max_accept]", accept.dim() == 2 and accept.shape[0] == cache.batch)
+    _int32(fn, "accept", accept, cache.device)
+    _int32(fn, "num_accept", num_accept, cache.device, (cache.batch,))
+    _int32(fn, "new_lens", new_lens, cache.device, (cache.batch,))
+    s = _launch_stream(fn, cache.device, stream)
+    _check(fn, load().fp_cache_commit(cache.ref, cu_tokens.data_ptr(), total_tokens, accept.data_ptr(),
+                                      num_accept.data_ptr(), accept.shape[1], new_lens.data_ptr(), s))
+
+
+class Tree:
+    """What stays the same from one ``fp_tree_attention`` call to the next: the
+    cache, the query heads, the row counts and the scratch buffer (one plan per
+    stream, and per captured graph that may run beside others)."""
+
+    def __init__(self, cache: Cache, hq: int, total_tokens: int, max_tokens: int, softmax_scale: float = 0.0):
+        self.cache = cache
+        self.hq, self.total_tokens = hq, total_tokens
+        self.p = TreeParams(hq=hq, total_tokens=total_tokens, max_tokens=max_tokens, softmax_scale=softmax_scale)
+        self.ref = ctypes.byref(self.p)
+        with torch.cuda.device(cache.device):
+            self.ws_bytes = load().fp_tree_workspace_size(cache.ref, self.ref)
+        if self.ws_bytes == 0:
+            raise FPError("fp_tree_workspace_size", -2)
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=cache.device)
+
+
+def fp_tree_attention(plan: Tree, cu_tokens, q, o, mask=None, lse=None, stream=None):
+    """Attention of the new tokens (q: bf16 [tokens, hq, d], any token stride)
+    over the cache into o (bf16, contiguous) and lse (float32 [hq, tokens]).
+    mask: int32 [tokens, words], bit j: the row sees new token j of its request;
+    without it a row sees the new tokens up to its own."""
+    fn, cache, p = "fp_tree_attention", plan.cache, plan.p
+    d = cache.head_dim
+    shape = (plan.total_tokens, plan.hq, d)
+    _int32(fn, "cu_tokens", cu_tokens, cache.device, (cache.batch + 1,))
+    _expect(fn, f"q must be bfloat16 {shape} on {cache.device}, contiguous within a token",
+            q.dtype is torch.bfloat16 and tuple(q.shape) == shape and q.device == cache.device and q.stride(2) == 1
+            and (q.stride(1) == d or plan.hq == 1))
+    _expect(fn, f"o must be contiguous bfloat16 {shape} on {cache.device}",
+            o.dtype is torch.bfloat16 and tuple(o.shape) == shape and o.device == cache.device and o.is_contiguous())
+    if lse is not None:
+        _expect(fn, f"lse must be contiguous float32 {(plan.hq, plan.total_tokens)} on {cache.device}",
+                lse.dtype is torch.float32 and tuple(lse.shape) == (plan.hq, plan.total_tokens)
+                and lse.device == cache.device and lse.is_contiguous())
+    if mask is not None:
+        _expect(fn, "mask must be [tokens, words]", mask.dim() == 2 and mask.shape[0] == plan.total_tokens)
+        _int32(fn, "mask", mask, cache.device)
+    s = _launch_stream(fn, cache.device, stream)
+    p.cu_tokens, p.mask, p.mask_words = cu_tokens.data_ptr(), _ptr(mask), 0 if mask is None else mask.shape[1]
+    p.q_stride = q.stride(0) if plan.total_tokens > 1 else 0
+    _check(fn, load().fp_tree_attention(cache.ref, plan.ref, q.data_ptr(), o.data_ptr(), _ptr(lse),
+                                        plan.workspace.data_ptr(), plan.ws_bytes, s))
 
 
 def run_path(p: Params, q, k, v, bufs: Buffers, paged: bool = False, fused: bool = True, stream=None):

@@ -27,20 +27,6 @@ fp_status_t cuda_fail(const char* step, cudaError_t e) {
   return FP_ERR_CUDA;
 }
 
-unsigned* status_ptr() {
-  static unsigned* ptrs[kMaxDevices] = {};
-  static std::mutex mu;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-  std::lock_guard<std::mutex> lk(mu);
-  if (!ptrs[dev]) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return nullptr;
-    ptrs[dev] = static_cast<unsigned*>(p);
-  }
-  return ptrs[dev];
-}
-
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
@@ -171,6 +157,21 @@ fp_status_t attention_impl(const fp_params_t* p, bool paged, const void* q, cons
 }
 
 }  // namespace
+
+unsigned* status_ptr() {
+  static unsigned* ptrs[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!ptrs[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return nullptr;
+    ptrs[dev] = static_cast<unsigned*>(p);
+  }
+  return ptrs[dev];
+}
+
 }  // namespace fp
 
 using namespace fp;

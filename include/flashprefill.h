@@ -16,6 +16,11 @@
  *      online softmax that visits only the listed KV blocks; all query heads of
  *      a KV group share each K/V tile (PackGQA); BF16 or FP8-e4m3; contiguous,
  *      varlen (continuous batching) or paged KV.
+ * Around it, the paged cache the prefill reads and the decoding steps after it:
+ *   4. fp_cache_write / fp_cache_read / fp_cache_commit -- put tokens into the
+ *      cache (quantising them), take them out, keep the accepted drafted ones.
+ *   5. fp_tree_attention -- attention of a tree of drafted tokens, or of single
+ *      tokens, over that cache.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -236,6 +241,130 @@ fp_status_t fp_discover_compact_static(const fp_params_t* p, const void* q, cons
 
 /* Size in bytes of the fixed scratch array fp_discover_compact_static uses. */
 size_t fp_static_scratch_bytes(void);
+
+/* ------------------------------------------------------------------------
+ * The paged cache and the decoding steps over it.
+ *
+ * fp_cache_t describes the same paged cache that fp_params_t does for the
+ * prefill calls: pools [num_pages, page_size, hkv, head_dim], the page table
+ * and the cached length of every request.
+ * - Formats: dtype FP_BF16 (scale FP_SCALE_NONE), or FP_E4M3 with float32
+ *   scales: FP_SCALE_HEAD, one per KV head (k_scale, v_scale: [hkv]; the format
+ *   that fp_prefill and fp_paged_sparse_prefill read, the scales given by the
+ *   caller), or FP_SCALE_TOKEN, one per token and KV head (k_scale, v_scale:
+ *   [num_pages, hkv, page_size]; written by fp_cache_write). The value of an
+ *   e4m3 code is code * scale.
+ * - head_dim 128, or 64 with FP_BF16; page_size a power of two in 16..65536.
+ *   Pools and scales are 16-byte aligned.
+ * - "New tokens": cu_tokens (device int32 [batch + 1], non-decreasing,
+ *   cu_tokens[0] >= 0) gives request r the n_r = cu[r+1] - cu[r] rows
+ *   cu[r] .. cu[r+1]-1 of the packed tensors, which have total_tokens rows.
+ *   They are the request's LAST n_r positions, kv_lens[r] - n_r ..
+ *   kv_lens[r] - 1 (kv_lens counts them; as in chunked prefill). n_r may be 0.
+ *   Packed rows outside every request are neither read nor written.
+ * - Checked on the device: a request whose cu_tokens or kv_lens do not fit
+ *   (n_r < 0, cu[r+1] > total_tokens, n_r > kv_lens[r], kv_lens[r] >
+ *   max_pages_per_req * page_size) sets FP_DEV_BAD_SEQLENS and is skipped; a
+ *   page id outside [0, num_pages) sets FP_DEV_BAD_PAGE, its tokens are not
+ *   written, and read as zeros.
+ * - A page may belong to several requests as long as no call writes a slot
+ *   twice or reads a slot that the same call writes.
+ */
+typedef enum { FP_SCALE_NONE = 0, FP_SCALE_HEAD = 1, FP_SCALE_TOKEN = 2 } fp_scale_t;
+
+typedef struct {
+  fp_dtype_t dtype;           /* element type of the pools */
+  fp_scale_t scale;           /* FP_SCALE_NONE with FP_BF16, HEAD or TOKEN with FP_E4M3 */
+  int batch;                  /* requests, 1..4096 */
+  int hkv;                    /* KV heads */
+  int head_dim;
+  int page_size;              /* tokens per page */
+  int num_pages;              /* pages in each pool */
+  int max_pages_per_req;      /* row length of page_table */
+  void* k_pool;               /* device [num_pages, page_size, hkv, head_dim] */
+  void* v_pool;
+  float* k_scale;             /* device, see above; NULL with FP_BF16 */
+  float* v_scale;
+  const int32_t* page_table;  /* device int32 [batch, max_pages_per_req] */
+  const int32_t* kv_lens;     /* device int32 [batch]: cached tokens, the call's new ones included */
+} fp_cache_t;
+
+/*
+ * Writes the new tokens' K and V (device bf16 [total_tokens, hkv, head_dim];
+ * k_stride, v_stride: elements between tokens, a multiple of 8 and at least
+ * hkv * head_dim, so that slices of a fused projection need no copy) into the
+ * cache. FP_E4M3: code = x / scale, clamped to +-448 and rounded to nearest
+ * even (NaN stays NaN); with FP_SCALE_TOKEN the scale of a token and head is
+ * the float32 max |x| / 448 over its head_dim values (0 for a zero row, whose
+ * codes are 0), and is stored beside the codes. FP_SCALE_HEAD reads the given
+ * scales; a head scale of 0 is taken as 1.
+ */
+fp_status_t fp_cache_write(const fp_cache_t* c, const int32_t* cu_tokens, int total_tokens, const void* k,
+                           long long k_stride, const void* v, long long v_stride, void* stream);
+
+/*
+ * Reads cached tokens back as bf16 rows (k, v: device bf16, strides as for
+ * fp_cache_write): code * scale in float32, rounded to nearest even. The rows
+ * of request r are its last n_r positions; starts (device int32 [batch] or
+ * NULL) makes them positions starts[r] .. starts[r] + n_r - 1 instead (within
+ * 0 .. kv_lens[r], else FP_DEV_BAD_SEQLENS). Rows on a bad page read as zeros.
+ */
+fp_status_t fp_cache_read(const fp_cache_t* c, const int32_t* cu_tokens, int total_tokens, const int32_t* starts,
+                          void* k, long long k_stride, void* v, long long v_stride, void* stream);
+
+/*
+ * Keeps the accepted ones of the new tokens: cached row base + accept[r][i]
+ * (base = kv_lens[r] - n_r; codes and token scales) moves to base + i for
+ * i = 0 .. num_accept[r] - 1, and new_lens[r] = base + num_accept[r]. accept:
+ * device int32 [batch, max_accept], strictly ascending indices in 0 .. n_r - 1
+ * (a root-to-leaf path of a tree in topological order). num_accept, new_lens:
+ * device int32 [batch]; new_lens may be the kv_lens array itself. A request
+ * whose list breaks these rules (FP_DEV_BAD_LIST) or touches a bad page
+ * (FP_DEV_BAD_PAGE) is left as it was, with new_lens[r] = kv_lens[r]; so is
+ * one with bad lengths. Rows behind the accepted ones keep what they held.
+ */
+fp_status_t fp_cache_commit(const fp_cache_t* c, const int32_t* cu_tokens, int total_tokens, const int32_t* accept,
+                            const int32_t* num_accept, int max_accept, int32_t* new_lens, void* stream);
+
+/* The queries of one fp_tree_attention call. */
+typedef struct {
+  int hq;                     /* query heads; hq / hkv in 1..8 or 16 */
+  int total_tokens;           /* rows of q and o */
+  int max_tokens;             /* upper bound of every n_r, 1..1024 */
+  float softmax_scale;        /* 0 -> 1 / sqrt(head_dim) */
+  long long q_stride;         /* elements between tokens of q, a multiple of 8; 0 -> hq * head_dim */
+  const int32_t* cu_tokens;   /* device int32 [batch + 1] */
+  const uint32_t* mask;       /* device [total_tokens, mask_words] or NULL (see below) */
+  int mask_words;             /* with a mask: at least ceil(max_tokens / 32) */
+} fp_tree_t;
+
+/* Bytes of device scratch fp_tree_attention needs (0: unsupported arguments).
+ * Depends on the SM count of the current device, not on any device array. */
+size_t fp_tree_workspace_size(const fp_cache_t* c, const fp_tree_t* t);
+
+/*
+ * Attention of the new tokens over the cache (write them first). Every row of
+ * request r sees the positions before base = kv_lens[r] - n_r; of the new
+ * tokens it sees number j iff bit j % 32 of word j / 32 of its mask row is set
+ * (its own token included only if its bit is; bits >= n_r are ignored).
+ * mask == NULL: row t sees the new tokens 0 .. t, which with n_r = 1 is plain
+ * decoding.
+ *   O[t, h] = sum_j softmax_j(scale * q_t,h . k_j) v_j,  lse = log sum exp
+ * q: device bf16 [total_tokens, hq, head_dim] (q_stride); o: device bf16
+ * [total_tokens, hq, head_dim], contiguous; lse: NULL or device float
+ * [hq, total_tokens] (natural log). A row that sees nothing gets O = 0 and
+ * lse = -inf. Cached values at positions a row does not see, and slots at or
+ * behind kv_lens[r], do not reach its result, whatever they hold (NaN and
+ * infinities too). Scores, softmax sums and O are float32; the weights enter
+ * O += P V as f16 (e4m3 caches), or as bf16 pairs hi + lo (bf16 caches).
+ * The keys of all requests are divided evenly over the SMs; partial results
+ * are combined in a fixed order, so equal calls give equal bits.
+ * A request with n_r > max_tokens sets FP_DEV_BAD_SEQLENS and is skipped.
+ * workspace: fp_tree_workspace_size bytes, 256-byte aligned, contents
+ * overwritten; calls that may overlap on the GPU need one each.
+ */
+fp_status_t fp_tree_attention(const fp_cache_t* c, const fp_tree_t* t, const void* q, void* o, float* lse,
+                              void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, writes the device status bits (FP_DEV_*) of the
