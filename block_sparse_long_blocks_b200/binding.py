@@ -322,16 +322,31 @@ def fp_get_device_status(stream=None) -> int:
 # the paged cache and the decoding steps over it
 # ----------------------------------------------------------------------------
 
-def _expect(fn: str, what: str, ok: bool):
-    if not ok:
-        raise ValueError(f"{fn}: {what}")
+# These calls run once per layer and step, on inputs of a few kilobytes, so what
+# they check per call is kept to comparisons (messages are built on failure).
+
+def _refuse(fn: str, what: str):
+    raise ValueError(f"{fn}: {what}")
 
 
-def _int32(fn: str, name: str, t: torch.Tensor, device, shape=None):
-    _expect(fn, f"{name} must be a contiguous int32 tensor on {device}"
-            + ("" if shape is None else f" of shape {tuple(shape)}"),
-            t.dtype is torch.int32 and t.device == device and t.is_contiguous()
-            and (shape is None or tuple(t.shape) == tuple(shape)))
+def _is_int32(t: torch.Tensor, dev: int, shape: tuple) -> bool:
+    return t.dtype is torch.int32 and t.get_device() == dev and t.shape == shape and t.is_contiguous()
+
+
+def _is_rows(t: torch.Tensor, dev: int, shape: tuple) -> bool:
+    """bf16 [tokens, heads, d] whose tokens are contiguous, at any distance."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != shape:
+        return False
+    s = t.stride()
+    return s[2] == 1 and (s[1] == shape[2] or shape[1] == 1)
+
+
+def _launch_stream(fn: str, dev: int, stream) -> int:
+    """The stream of a call whose tensors live on device `dev`: launches go to the
+    current device, so the two have to agree."""
+    if torch.cuda.current_device() != dev:
+        _refuse(fn, f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 class Cache:
@@ -343,29 +358,30 @@ class Cache:
     head, written by ``fp_cache_write``). Holds the tensors; copies nothing."""
 
     def __init__(self, k_pool, v_pool, page_table, kv_lens, k_scale=None, v_scale=None):
-        fn = "Cache"
-        _expect(fn, "pools must be 4-D [pages, page, hkv, d], contiguous, of one shape, type and device",
-                k_pool.dim() == 4 and k_pool.shape == v_pool.shape and k_pool.dtype == v_pool.dtype
-                and k_pool.device == v_pool.device and k_pool.is_contiguous() and v_pool.is_contiguous())
-        _expect(fn, "pools must be bfloat16 or float8_e4m3fn",
-                k_pool.dtype in (torch.bfloat16, torch.float8_e4m3fn))
+        if not (k_pool.dim() == 4 and k_pool.shape == v_pool.shape and k_pool.dtype == v_pool.dtype
+                and k_pool.device == v_pool.device and k_pool.is_contiguous() and v_pool.is_contiguous()):
+            _refuse("Cache", "pools must be 4-D [pages, page, hkv, d], contiguous, of one shape, type and device")
+        if k_pool.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            _refuse("Cache", "pools must be bfloat16 or float8_e4m3fn")
         pages, page, hkv, d = k_pool.shape
-        _expect(fn, "page_table must be 2-D", page_table.dim() == 2)
-        _int32(fn, "page_table", page_table, k_pool.device)
-        _int32(fn, "kv_lens", kv_lens, k_pool.device, (page_table.shape[0],))
+        self.dev = dev = k_pool.get_device()
+        if page_table.dim() != 2 or not _is_int32(page_table, dev, tuple(page_table.shape)):
+            _refuse("Cache", "page_table must be a contiguous int32 [batch, max_pages] on the pools' device")
+        if not _is_int32(kv_lens, dev, (page_table.shape[0],)):
+            _refuse("Cache", "kv_lens must be a contiguous int32 [batch] on the pools' device")
         scale = FP_SCALE_NONE
         if k_pool.dtype is torch.float8_e4m3fn:
-            _expect(fn, "e4m3 pools need k_scale and v_scale", k_scale is not None and v_scale is not None)
+            if k_scale is None or v_scale is None:
+                _refuse("Cache", "e4m3 pools need k_scale and v_scale")
             scale = FP_SCALE_TOKEN if k_scale.dim() == 3 else FP_SCALE_HEAD
             shape = (pages, hkv, page) if scale == FP_SCALE_TOKEN else (hkv,)
             for s in (k_scale, v_scale):
-                _expect(fn, f"scales must be contiguous float32 [hkv] or [pages, hkv, page], here {shape}",
-                        tuple(s.shape) == shape and s.dtype is torch.float32 and s.device == k_pool.device
-                        and s.is_contiguous())
-        else:
-            _expect(fn, "bf16 pools take no scales", k_scale is None and v_scale is None)
+                if not (s.shape == shape and s.dtype is torch.float32 and s.get_device() == dev and s.is_contiguous()):
+                    _refuse("Cache", f"scales must be contiguous float32 [hkv] or [pages, hkv, page], here {shape}")
+        elif k_scale is not None or v_scale is not None:
+            _refuse("Cache", "bf16 pools take no scales")
         self.tensors = (k_pool, v_pool, page_table, kv_lens, k_scale, v_scale)
-        self.device, self.hkv, self.head_dim, self.batch = k_pool.device, hkv, d, page_table.shape[0]
+        self.hkv, self.head_dim, self.batch = hkv, d, page_table.shape[0]
         self.p = CacheParams(
             dtype=FP_BF16 if scale == FP_SCALE_NONE else FP_E4M3, scale=scale, batch=self.batch, hkv=hkv, head_dim=d,
             page_size=page, num_pages=pages, max_pages_per_req=page_table.shape[1], k_pool=k_pool.data_ptr(),
@@ -374,59 +390,53 @@ class Cache:
         self.ref = ctypes.byref(self.p)
 
 
-def _launch_stream(fn: str, device, stream) -> int:
-    """The stream of a call whose tensors live on `device`: launches go to the
-    current device, so the two have to agree."""
-    _expect(fn, f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}",
-            device.index == torch.cuda.current_device())
-    return _stream(stream)
-
-
 def _rows(fn: str, cache: Cache, cu, k, v):
-    _int32(fn, "cu_tokens", cu, cache.device, (cache.batch + 1,))
-    for x in (k, v):
-        _expect(fn, f"k and v must be bfloat16 [tokens, {cache.hkv}, {cache.head_dim}] on {cache.device}, "
-                "contiguous within a token",
-                x.dtype is torch.bfloat16 and x.dim() == 3 and x.shape[1] == cache.hkv
-                and x.shape[2] == cache.head_dim and x.shape[0] == k.shape[0] and x.device == cache.device
-                and x.stride(2) == 1 and (x.stride(1) == cache.head_dim or cache.hkv == 1))
+    dev = cache.dev
+    if not _is_int32(cu, dev, (cache.batch + 1,)):
+        _refuse(fn, f"cu_tokens must be a contiguous int32 [{cache.batch + 1}] on cuda:{dev}")
     total = k.shape[0]
-    row = cache.hkv * cache.head_dim
-    # (the stride of a single row is whatever its tensor happens to say)
-    return total, *(x.stride(0) if total > 1 else row for x in (k, v))
+    shape = (total, cache.hkv, cache.head_dim)
+    if not (_is_rows(k, dev, shape) and _is_rows(v, dev, shape)):
+        _refuse(fn, f"k and v must be bfloat16 [tokens, {cache.hkv}, {cache.head_dim}] on cuda:{dev}, "
+                "contiguous within a token")
+    if total > 1:
+        return total, k.stride(0), v.stride(0)
+    row = cache.hkv * cache.head_dim  # (the stride of a single row is whatever its tensor happens to say)
+    return total, row, row
 
 
 def fp_cache_write(cache: Cache, cu_tokens, k, v, stream=None):
     """Writes new tokens' K and V (bf16 [tokens, hkv, d], any token stride) into the cache."""
     total, ks, vs = _rows("fp_cache_write", cache, cu_tokens, k, v)
-    s = _launch_stream("fp_cache_write", cache.device, stream)
-    _check("fp_cache_write", load().fp_cache_write(cache.ref, cu_tokens.data_ptr(), total, k.data_ptr(), ks,
-                                                   v.data_ptr(), vs, s))
+    s = _launch_stream("fp_cache_write", cache.dev, stream)
+    code = load().fp_cache_write(cache.ref, cu_tokens.data_ptr(), total, k.data_ptr(), ks, v.data_ptr(), vs, s)
+    _check("fp_cache_write", code)
 
 
 def fp_cache_read(cache: Cache, cu_tokens, k, v, starts=None, stream=None):
     """Reads cached tokens into k and v (bf16 [tokens, hkv, d]): the last ones of
     every request, or those from ``starts`` on."""
     total, ks, vs = _rows("fp_cache_read", cache, cu_tokens, k, v)
-    if starts is not None:
-        _int32("fp_cache_read", "starts", starts, cache.device, (cache.batch,))
-    s = _launch_stream("fp_cache_read", cache.device, stream)
-    _check("fp_cache_read", load().fp_cache_read(cache.ref, cu_tokens.data_ptr(), total, _ptr(starts), k.data_ptr(),
-                                                 ks, v.data_ptr(), vs, s))
+    if starts is not None and not _is_int32(starts, cache.dev, (cache.batch,)):
+        _refuse("fp_cache_read", f"starts must be a contiguous int32 [{cache.batch}] on cuda:{cache.dev}")
+    s = _launch_stream("fp_cache_read", cache.dev, stream)
+    code = load().fp_cache_read(cache.ref, cu_tokens.data_ptr(), total, _ptr(starts), k.data_ptr(), ks, v.data_ptr(),
+                                vs, s)
+    _check("fp_cache_read", code)
 
 
 def fp_cache_commit(cache: Cache, cu_tokens, total_tokens: int, accept, num_accept, new_lens, stream=None):
     """Moves the accepted new tokens' rows to the positions they keep and writes
     the requests' new lengths (``new_lens`` may be the cache's kv_lens)."""
-    fn = "fp_cache_commit"
-    _int32(fn, "cu_tokens", cu_tokens, cache.device, (cache.batch + 1,))
-    _expect(fn, f"accept must be [{cache.batch}, max_accept]", accept.dim() == 2 and accept.shape[0] == cache.batch)
-    _int32(fn, "accept", accept, cache.device)
-    _int32(fn, "num_accept", num_accept, cache.device, (cache.batch,))
-    _int32(fn, "new_lens", new_lens, cache.device, (cache.batch,))
-    s = _launch_stream(fn, cache.device, stream)
-    _check(fn, load().fp_cache_commit(cache.ref, cu_tokens.data_ptr(), total_tokens, accept.data_ptr(),
-                                      num_accept.data_ptr(), accept.shape[1], new_lens.data_ptr(), s))
+    fn, dev, R = "fp_cache_commit", cache.dev, cache.batch
+    if not (_is_int32(cu_tokens, dev, (R + 1,)) and _is_int32(num_accept, dev, (R,)) and _is_int32(new_lens, dev, (R,))
+            and accept.dim() == 2 and _is_int32(accept, dev, (R, accept.shape[1]))):
+        _refuse(fn, f"cu_tokens [{R + 1}], accept [{R}, max_accept], num_accept [{R}] and new_lens [{R}] must be "
+                f"contiguous int32 on cuda:{dev}")
+    s = _launch_stream(fn, dev, stream)
+    code = load().fp_cache_commit(cache.ref, cu_tokens.data_ptr(), total_tokens, accept.data_ptr(),
+                                  num_accept.data_ptr(), accept.shape[1], new_lens.data_ptr(), s)
+    _check(fn, code)
 
 
 class Tree:
@@ -437,13 +447,17 @@ class Tree:
     def __init__(self, cache: Cache, hq: int, total_tokens: int, max_tokens: int, softmax_scale: float = 0.0):
         self.cache = cache
         self.hq, self.total_tokens = hq, total_tokens
+        self.shape, self.lse_shape = (total_tokens, hq, cache.head_dim), (hq, total_tokens)
         self.p = TreeParams(hq=hq, total_tokens=total_tokens, max_tokens=max_tokens, softmax_scale=softmax_scale)
         self.ref = ctypes.byref(self.p)
-        with torch.cuda.device(cache.device):
+        if cache.dev < 0:
+            _refuse("Tree", "the cache must be on a CUDA device")
+        with torch.cuda.device(cache.dev):
             self.ws_bytes = load().fp_tree_workspace_size(cache.ref, self.ref)
         if self.ws_bytes == 0:
             raise FPError("fp_tree_workspace_size", -2)
-        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=cache.device)
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=f"cuda:{cache.dev}")
+        self.ws_ptr = self.workspace.data_ptr()
 
 
 def fp_tree_attention(plan: Tree, cu_tokens, q, o, mask=None, lse=None, stream=None):
@@ -452,26 +466,30 @@ def fp_tree_attention(plan: Tree, cu_tokens, q, o, mask=None, lse=None, stream=N
     mask: int32 [tokens, words], bit j: the row sees new token j of its request;
     without it a row sees the new tokens up to its own."""
     fn, cache, p = "fp_tree_attention", plan.cache, plan.p
-    d = cache.head_dim
-    shape = (plan.total_tokens, plan.hq, d)
-    _int32(fn, "cu_tokens", cu_tokens, cache.device, (cache.batch + 1,))
-    _expect(fn, f"q must be bfloat16 {shape} on {cache.device}, contiguous within a token",
-            q.dtype is torch.bfloat16 and tuple(q.shape) == shape and q.device == cache.device and q.stride(2) == 1
-            and (q.stride(1) == d or plan.hq == 1))
-    _expect(fn, f"o must be contiguous bfloat16 {shape} on {cache.device}",
-            o.dtype is torch.bfloat16 and tuple(o.shape) == shape and o.device == cache.device and o.is_contiguous())
+    dev, shape = cache.dev, plan.shape
+    if not _is_int32(cu_tokens, dev, (cache.batch + 1,)):
+        _refuse(fn, f"cu_tokens must be a contiguous int32 [{cache.batch + 1}] on cuda:{dev}")
+    if not _is_rows(q, dev, shape):
+        _refuse(fn, f"q must be bfloat16 {shape} on cuda:{dev}, contiguous within a token")
+    if not (o.dtype is torch.bfloat16 and o.get_device() == dev and o.shape == shape and o.is_contiguous()):
+        _refuse(fn, f"o must be contiguous bfloat16 {shape} on cuda:{dev}")
+    lse_ptr = mask_ptr = None
+    words = 0
     if lse is not None:
-        _expect(fn, f"lse must be contiguous float32 {(plan.hq, plan.total_tokens)} on {cache.device}",
-                lse.dtype is torch.float32 and tuple(lse.shape) == (plan.hq, plan.total_tokens)
-                and lse.device == cache.device and lse.is_contiguous())
+        if not (lse.dtype is torch.float32 and lse.get_device() == dev and lse.shape == plan.lse_shape
+                and lse.is_contiguous()):
+            _refuse(fn, f"lse must be contiguous float32 {plan.lse_shape} on cuda:{dev}")
+        lse_ptr = lse.data_ptr()
     if mask is not None:
-        _expect(fn, "mask must be [tokens, words]", mask.dim() == 2 and mask.shape[0] == plan.total_tokens)
-        _int32(fn, "mask", mask, cache.device)
-    s = _launch_stream(fn, cache.device, stream)
-    p.cu_tokens, p.mask, p.mask_words = cu_tokens.data_ptr(), _ptr(mask), 0 if mask is None else mask.shape[1]
-    p.q_stride = q.stride(0) if plan.total_tokens > 1 else 0
-    _check(fn, load().fp_tree_attention(cache.ref, plan.ref, q.data_ptr(), o.data_ptr(), _ptr(lse),
-                                        plan.workspace.data_ptr(), plan.ws_bytes, s))
+        if mask.dim() != 2 or not _is_int32(mask, dev, (shape[0], mask.shape[1])):
+            _refuse(fn, f"mask must be contiguous int32 [{shape[0]}, words] on cuda:{dev}")
+        mask_ptr, words = mask.data_ptr(), mask.shape[1]
+    s = _launch_stream(fn, dev, stream)
+    p.cu_tokens, p.mask, p.mask_words = cu_tokens.data_ptr(), mask_ptr, words
+    p.q_stride = q.stride(0) if shape[0] > 1 else 0
+    code = load().fp_tree_attention(cache.ref, plan.ref, q.data_ptr(), o.data_ptr(), lse_ptr, plan.ws_ptr,
+                                    plan.ws_bytes, s)
+    _check(fn, code)
 
 
 def run_path(p: Params, q, k, v, bufs: Buffers, paged: bool = False, fused: bool = True, stream=None):

@@ -9,16 +9,15 @@
 //
 // What bounds it: every cached row is read once per M-tile of 16 or 32 rows,
 // 4 * rows flops per element, so up to ~250 rows (bf16) HBM is the floor. The
-// keys of ALL requests, KV heads and M-tiles form one axis of 128-key tiles,
-// cut evenly over one persistent CTA per SM, however ragged the lengths. A unit
+// keys of ALL requests, KV heads and M-tiles form one axis of tiles (32 KB of K:
+// 128 keys of 256 bytes, or 256 of 128), cut evenly over one persistent CTA per SM, however ragged the lengths. A unit
 // (request, KV head, M-tile) that lies within one CTA's share is finished there;
 // the others leave normalised partial rows (float32 O, base-2 lse) in the
 // workspace, at most two per CTA, which a second kernel (a programmatic
 // dependent launch) combines in a fixed order: O = sum_i 2^(lse_i - lse) O_i.
 //
 // A CTA: warp 8 issues TMA copies of K and V tiles (4-D boxes per page, 128-byte
-// swizzle, and the tile's token scales) into a ring of 32 KB (bf16) or 16 KB
-// (e4m3) slots; warps 0-7 hold the M-tiles' rows as mma.sync fragments (16 rows
+// swizzle, and the tile's token scales) into a ring of five 32 KB slots; warps 0-7 hold the M-tiles' rows as mma.sync fragments (16 rows
 // per warp) and split the tile's keys, so no warp waits for another until the
 // unit's end, where the key groups' (m, l, O) meet in shared memory.
 // mma.sync and not tcgen05 here: 8 or 16 useful rows would fill a sixteenth or
@@ -42,6 +41,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.cuh"
 #include "sm100.cuh"
@@ -50,18 +50,17 @@ namespace fp {
 
 namespace {
 
-constexpr int kTile = 128;                     // keys per tile
 constexpr int kWarps = 8;                      // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kConsumers = kWarps * 32;
-constexpr int kSplitGroup = 16 * kWarps;
-static_assert(kTile == kSplitGroup, "one 16-key step per warp and tile when a single M-tile is held");
+constexpr int kTileBytes = 32 * 1024;          // of K, and of V
 
 struct TreeArgs {
   CacheGeometry g;
   int Hq, G;
   int max_tokens;
   int rows;               // rows per M-tile unit
+  int tile;               // keys per tile
   const uint32_t* mask;
   int mask_words;
   const __nv_bfloat16* q;
@@ -87,7 +86,7 @@ __device__ __forceinline__ void request_tiles(const TreeArgs& a, int r, int& off
     n = 0;
   }
   if (n == 0) return;
-  nt = (kv + kTile - 1) / kTile;
+  nt = (kv + a.tile - 1) / a.tile;
   nm = (n * a.G + a.rows - 1) / a.rows;
 }
 
@@ -171,36 +170,44 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+template <int OFF>
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr), "n"(OFF));
 }
+template <int OFF>
 __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr), "n"(OFF));
 }
 
 // c += A (16 x 16, row) * B (16 x 8, col), float32 accumulators
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   } else {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 }
 
-__device__ __forceinline__ uint32_t widen_e4m3(uint32_t two_bytes) {
+// The low or high pair of four e4m3 codes -> two f16 (exact).
+__device__ __forceinline__ uint32_t widen_lo(uint32_t x) {
   uint32_t u;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"((unsigned short)two_bytes));
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(u) : "r"(x));
+  return u;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
+  uint32_t u;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(u) : "r"(x));
   return u;
 }
 
@@ -220,15 +227,16 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t u) {
 template <bool E4M3, int D>
 struct Cfg {
   static constexpr int ES = E4M3 ? 1 : 2;
+  static constexpr int TILE = kTileBytes / (D * ES);     // keys per tile: 128 or 256
   static constexpr int CHUNKS = D * ES / 128;            // 128-byte chunks of a row
   static constexpr int CH_ELEMS = 128 / ES;
-  static constexpr int CHUNK = kTile * 128;              // bytes of a tile's chunk
-  static constexpr int DATA = CHUNKS * CHUNK;
-  static constexpr int SLOT = DATA + (E4M3 ? 1024 : 0);  // + the tile's 128 token scales (slots stay 1024-aligned)
+  static constexpr int CHUNK = TILE * 128;               // bytes of a tile's chunk
+  static constexpr int SLOT = kTileBytes + (E4M3 ? 1024 : 0);  // + the tile's token scales
   static constexpr int RED = 4 * 16 * D * 4;             // four key groups' O of 16 rows
-  static constexpr int SLOTS = (E4M3 ? 160 : 160) * 1024 / SLOT;
+  static constexpr int SLOTS = 5;
   static constexpr int SMEM_FIXED = 1024 + SLOTS * SLOT + RED + 2 * kWarps * 16 * 4 + 2 * SLOTS * 8 + 64;
   static_assert(D * ES % 128 == 0, "head dim 128, or 64 with bf16");
+  static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -240,6 +248,40 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
+// Infinities and NaN that new tokens of this segment hold in four columns of V
+// reach the rows that see them (rare: they entered the products as zeros).
+template <bool E4M3, bool TOKEN, int D>
+__device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg, int t, int d, int tile, float4& acc) {
+  const CacheGeometry& g = a.g;
+  const int32_t* row = g.table + (long long)sg.r * g.max_pages;
+  for (int pos = max(sg.base, sg.t0 * tile); pos < min(sg.kv, sg.t1 * tile); ++pos) {
+    const int j = pos - sg.base;
+    const bool see = a.mask ? (__ldg(a.mask + (long long)(sg.off + t) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u : j <= t;
+    const int page = __ldg(row + (pos >> g.page_shift));
+    if (!see || page < 0 || page >= g.num_pages) continue;
+    const long long slot = ((long long)page << g.page_shift) + (pos & (g.page_size - 1));
+    const long long at = (slot * g.Hkv + sg.head) * D + d;
+    float v[4];
+    if constexpr (E4M3) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(g.v_pool + at);
+      float sc = 1.f;
+      if (TOKEN) sc = __ldg(g.v_scale + (((long long)page * g.Hkv + sg.head) << g.page_shift) + (pos & (g.page_size - 1)));
+      const __half2_raw lo = {(unsigned short)widen_lo(w), (unsigned short)(widen_lo(w) >> 16)};
+      const __half2_raw hi = {(unsigned short)widen_hi(w), (unsigned short)(widen_hi(w) >> 16)};
+      const float2 x = __half22float2(__half2(lo)), y = __half22float2(__half2(hi));
+      v[0] = x.x * sc, v[1] = x.y * sc, v[2] = y.x * sc, v[3] = y.y * sc;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(g.v_pool + at * 2);
+      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+    }
+    if (!isfinite(v[0])) acc.x += v[0];
+    if (!isfinite(v[1])) acc.y += v[1];
+    if (!isfinite(v[2])) acc.z += v[2];
+    if (!isfinite(v[3])) acc.w += v[3];
+  }
+}
+
 // E4M3: cache type; TOKEN: token scales; WM: M-tiles of 16 rows held by the CTA
 // (8 / WM warps split the keys of each).
 template <bool E4M3, bool TOKEN, int D, int WM>
@@ -247,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
   using C = Cfg<E4M3, D>;
   constexpr int KG = kWarps / WM;        // key groups
-  constexpr int STEPS = kTile / KG / 16;  // 16-key steps per warp and tile
+  constexpr int STEPS_ALL = C::TILE / KG / 16;         // 16-key steps per warp and tile,
+  constexpr int STEPS = STEPS_ALL < 2 ? STEPS_ALL : 2;  // of which so many share a softmax update
   constexpr int NT = D / 8;              // 8-column tiles of O
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -259,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* misc = reinterpret_cast<int*>(empty + C::SLOTS);
   volatile int* abort_flag = misc;
   int* warp_sum = misc + 1;                     // [9]
+  volatile int* s_odd = misc + 10;              // [2], by segment parity: see below
   int* pre = misc + 16;                         // [R + 1]
 
   const CacheGeometry& g = a.g;
@@ -271,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(empty + s, kWarps);
     }
     *abort_flag = 0;
+    s_odd[0] = s_odd[1] = 0;
     fence_barrier_init();
   }
   prefix_tiles(a, pre, warp_sum);  // (its barriers publish the initialisation above)
@@ -286,8 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    const int sub_rows = min(g.page_size, kTile);
-    const int sub_max = kTile / sub_rows;  // <= 8
+    const int sub_rows = min(g.page_size, C::TILE);
+    const int sub_max = C::TILE / sub_rows;  // <= 16
     int slot = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -296,16 +341,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment sg = segment_at(a, pre, x, x_end, r);
       const int32_t* row = g.table + (long long)sg.r * g.max_pages;
       auto page_at = [&](int tile) {  // the page of this lane's part of a tile
-        const int tok = tile * kTile + lane * sub_rows;
+        const int tok = tile * C::TILE + lane * sub_rows;
         return (lane < sub_max && tok < sg.kv) ? __ldg(row + (tok >> g.page_shift)) : -1;
       };
       int next_page = page_at(sg.t0);
       for (int t = sg.t0; t < sg.t1 && ok; ++t) {
         int page = next_page;
         if (t + 1 < sg.t1) next_page = page_at(t + 1);
-        const int tok = t * kTile + lane * sub_rows;
+        const int tok = t * C::TILE + lane * sub_rows;
         const bool mine = lane < sub_max && tok < sg.kv;
-        const int subs = min(sub_max, (sg.kv - t * kTile + sub_rows - 1) / sub_rows);
+        const int subs = min(sub_max, (sg.kv - t * C::TILE + sub_rows - 1) / sub_rows);
         bool bad = mine && (page < 0 || page >= g.num_pages);
         if (bad) {
           atomicOr(g.status, FP_DEV_BAD_PAGE);
@@ -332,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (TOKEN) {
               const float* sc = which ? g.v_scale : g.k_scale;
               const long long pg = bad ? 0 : page;  // (a bad page's codes are zeros: any scale does)
-              bulk_load(dst + C::DATA + lane * sub_rows * 4,
+              bulk_load(dst + kTileBytes + lane * sub_rows * 4,
                         sc + ((pg * g.Hkv + sg.head) << g.page_shift) + at, (uint32_t)sub_rows * 4u, full + slot);
             }
           }
@@ -358,13 +403,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ------------------------------------------------------------------ consumers
   const int mt = warp / KG, kg = warp % KG;
   const int gr = lane >> 2, c = lane & 3;  // fragment row and column group
-  uint32_t ringa = smem_u32(ring);
+  // ldmatrix addresses relative to a slot: slots are 1024-aligned, so the
+  // 128-byte swizzle of granule 2 i + hi of row `key` is an exclusive or with i << 5
+  uint32_t k_lane, v_lane;
+  {
+    const int kk = ((lane >> 4) << 3) + (lane & 7), khi = (lane >> 3) & 1;   // K: lanes 16-31 hold keys 8-15
+    const int vk = (((lane >> 3) & 1) << 3) + (lane & 7), vhi = lane >> 4;  // V: lanes 8-15 and 24-31 do
+    k_lane = smem_u32(ring) + (kg * STEPS_ALL * 16 + kk) * 128 + (((khi ^ kk) & 7) << 4);
+    v_lane = smem_u32(ring) + (kg * STEPS_ALL * 16 + vk) * 128 + (((vhi ^ vk) & 7) << 4);
+  }
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
   int r = request_of(pre, g.R, x_begin);
-  bool first_segment = true;
-  for (int x = x_begin; x < x_end;) {
+  int segment = 0;
+  for (int x = x_begin; x < x_end; ++segment) {
     const Segment sg = segment_at(a, pre, x, x_end, r);
     x += sg.t1 - sg.t0;
     const int nrows = sg.n * a.G;
@@ -415,8 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float v_mul = 1.f;  // what O is multiplied by at the end
     if (E4M3 && !TOKEN) {
       const float ks = __ldg(g.k_scale + sg.head);
-      sl2[0] *= ks;
-      sl2[1] *= ks;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sl2[i] *= ks;
+        if (sl2[i] == 0.f) sl2[i] = 1.2e-38f;  // (0 * -inf of a masked key would be NaN)
+      }
       v_mul = __ldg(g.v_scale + sg.head);
     }
 
@@ -425,35 +481,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float v_ref = 0.f;  // token scales: power of two above the largest v_scale so far (0: none yet)
+    // m: running maximum of the unscaled scores; ref = m * sl2 rounded, the exponents' reference
+    float m[2] = {-INFINITY, -INFINITY}, ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
 
-    for (int t = sg.t0; t < sg.t1; ++t) {
-      const int kslot = slot, vslot = slot + 1 == C::SLOTS ? 0 : slot + 1;
-      const uint32_t kphase = phase, vphase = vslot == 0 ? phase ^ 1u : phase;
-      slot = vslot + 1 == C::SLOTS ? 0 : vslot + 1;
-      phase = slot == 0 ? vphase ^ 1u : vphase;
-      uint32_t pf[STEPS][4], pl[STEPS][4];
-      uint32_t vm[STEPS][2];  // V rows that enter the product, as masks of key pairs
-      const bool special = (t + 1) * kTile > sg.base;  // holds new tokens, or slots behind the last
+    auto row_sees = [&](int i, int j) -> bool {  // row rho[i], new token j
+      return a.mask ? (__ldg(a.mask + (long long)(sg.off + tok[i]) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u
+                    : j <= tok[i];
+    };
 
-      if (ok) ok = mbar_wait<true>(full + kslot, kphase, abort_flag, g.status, FP_DEV_TIMEOUT);
-      const uint32_t ka = ringa + kslot * C::SLOT;
-      const float* ksc = reinterpret_cast<const float*>(ring + kslot * C::SLOT + C::DATA);
+    // STEPS steps of 16 keys of one tile: first position pos0, first key k0 of the
+    // tile; SPECIAL: some are new tokens, or slots behind the last one.
+    auto update = [&](auto special, int pos0, int k0, uint32_t ka, uint32_t va, const float* ksc, const float* vsc,
+                      uint64_t* vfull, uint32_t vphase) {
+      constexpr bool SPECIAL = decltype(special)::value;
       float s[STEPS][2][4];
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
-        const int k0 = (kg * STEPS + st) * 16;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[st][0][e] = s[st][1][e] = 0.f;
-        const int key = k0 + ((lane >> 4) << 3) + (lane & 7);
-        const uint32_t rowa = ka + key * 128;
-        const uint32_t sw = key & 7, hi = (lane >> 3) & 1;
+        const uint32_t rowa = ka + st * (16 * 128);
         if constexpr (!E4M3) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t b[4];
-            ldsm4(b, rowa + (ks / 4) * C::CHUNK + ((((ks & 3) * 2 + hi) ^ sw) << 4));
+            if (ks < 4) ldsm4<0>(b, rowa ^ ((ks & 3) << 5));
+            else ldsm4<C::CHUNK>(b, rowa ^ ((ks & 3) << 5));
             mma16816<false>(s[st][0], qf[ks], b[0], b[1]);
             mma16816<false>(s[st][1], qf[ks], b[2], b[3]);
           }
@@ -461,157 +514,154 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) {
             uint32_t b[4];  // (keys 0-7, granules 2kk and 2kk + 1), (keys 8-15, the same)
-            ldsm4(b, rowa + (((kk * 2 + hi) ^ sw) << 4));
-            mma16816<true>(s[st][0], qf[2 * kk], widen_e4m3(b[0]), widen_e4m3(b[0] >> 16));
-            mma16816<true>(s[st][1], qf[2 * kk], widen_e4m3(b[2]), widen_e4m3(b[2] >> 16));
-            mma16816<true>(s[st][0], qf[2 * kk + 1], widen_e4m3(b[1]), widen_e4m3(b[1] >> 16));
-            mma16816<true>(s[st][1], qf[2 * kk + 1], widen_e4m3(b[3]), widen_e4m3(b[3] >> 16));
+            ldsm4<0>(b, rowa ^ (kk << 5));
+            mma16816<true>(s[st][0], qf[2 * kk], widen_lo(b[0]), widen_hi(b[0]));
+            mma16816<true>(s[st][1], qf[2 * kk], widen_lo(b[2]), widen_hi(b[2]));
+            mma16816<true>(s[st][0], qf[2 * kk + 1], widen_lo(b[1]), widen_hi(b[1]));
+            mma16816<true>(s[st][1], qf[2 * kk + 1], widen_lo(b[3]), widen_hi(b[3]));
           }
         }
-        // scale; this thread's keys are k0 + 8 nt + 2c + {0, 1} (elements 0, 1: row gr; 2, 3: row gr + 8)
+      }
+      // this thread's keys are 16 st + 8 nt + 2c + {0, 1} (elements 0, 1: row gr; 2, 3: row gr + 8)
+      uint32_t vm[STEPS][2];  // V rows that enter the product, as masks of key pairs
+      float mx[2] = {m[0], m[1]};
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-          float2 kf = make_float2(1.f, 1.f);
-          if (TOKEN) kf = *reinterpret_cast<const float2*>(ksc + k0 + nt * 8 + 2 * c);
+          if constexpr (TOKEN) {
+            const float2 kf = *reinterpret_cast<const float2*>(ksc + k0 + st * 16 + nt * 8 + 2 * c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[st][nt][e] *= TOKEN ? sl2[e >> 1] * ((e & 1) ? kf.y : kf.x) : sl2[e >> 1];
-        }
-        vm[st][0] = vm[st][1] = 0xffffffffu;
-        if (special) {
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+            for (int e = 0; e < 4; ++e) s[st][nt][e] *= (e & 1) ? kf.y : kf.x;
+          }
+          if constexpr (SPECIAL) {
+            vm[st][nt] = 0xffffffffu;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int pos = t * kTile + k0 + nt * 8 + 2 * c + e;
+              const int pos = pos0 + st * 16 + nt * 8 + 2 * c + e;
               const int j = pos - sg.base;
               if (pos >= sg.kv) vm[st][nt] &= e ? 0x0000ffffu : 0xffff0000u;
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 bool see = j < 0;
-                if (j >= 0 && j < sg.n && in[i])
-                  see = a.mask ? (__ldg(a.mask + (long long)(sg.off + tok[i]) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u
-                               : j <= tok[i];
+                if (j >= 0 && j < sg.n && in[i]) see = row_sees(i, j);
                 if (!see) s[st][nt][2 * i + e] = -INFINITY;
               }
             }
-        }
-      }
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(empty + kslot);
-
-      // ---- softmax
-      float mx[2] = {m[0], m[1]};
-#pragma unroll
-      for (int st = 0; st < STEPS; ++st)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[st][nt][e]);
+        }
+
+      // ---- softmax
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
       }
-      float f[2] = {1.f, 1.f};
-      bool grew = false;
+      if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+        float f[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (mx[i] > m[i]) {
-          f[i] = exp2_fast(m[i] - mx[i]);
-          m[i] = mx[i];
+        for (int i = 0; i < 2; ++i) {
+          const float nref = mx[i] * sl2[i];
+          f[i] = mx[i] > m[i] ? exp2_fast(ref[i] - nref) : 1.f;
+          if (mx[i] > m[i]) {
+            m[i] = mx[i];
+            ref[i] = nref;
+          }
           l[i] *= f[i];
-          grew = true;
         }
-      if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[i][e] *= f[e >> 1];
       }
-      // reference of the exponent: the running maximum, 2^14 below it for f16 weights
+      // weights relative to the running maximum; f16 ones to 2^14 above it
       float neg[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) neg[i] = m[i] == -INFINITY ? 0.f : (E4M3 ? 14.f - m[i] : -m[i]);
+      for (int i = 0; i < 2; ++i) neg[i] = ref[i] == -INFINITY ? 0.f : (E4M3 ? 14.f - ref[i] : -ref[i]);
 
-      if (ok) ok = mbar_wait<true>(full + vslot, vphase, abort_flag, g.status, FP_DEV_TIMEOUT);
-      const uint32_t va = ringa + vslot * C::SLOT;
-      const float* vsc = reinterpret_cast<const float*>(ring + vslot * C::SLOT + C::DATA);
+      if (ok) ok = mbar_wait<true>(vfull, vphase, abort_flag, g.status, FP_DEV_TIMEOUT);
+      float inv_ref = 1.f;
       if constexpr (TOKEN) {
-        // the warp's largest finite v_scale among cached keys
-        float top = 0.f;
-        for (int st = 0; st < STEPS; ++st) {
-          const int k = (kg * STEPS + st) * 16 + (lane & 15);
-          const float y = vsc[k];
-          if (t * kTile + k < sg.kv && y < 3.0e38f) top = fmaxf(top, y);
+        // the largest v_scale of these keys (scales are not negative: they compare as integers)
+        uint32_t top = 0;
+        if (STEPS == 2 || lane < 16) top = __float_as_uint(vsc[k0 + lane]);
+        if constexpr (SPECIAL) {  // not those of slots behind the last token, or of new tokens without a finite one
+          const int pos = pos0 + lane;
+          if (pos >= sg.kv || (pos >= sg.base && top >= 0x7f800000u)) top = 0;
         }
-#pragma unroll
-        for (int sh = 8; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
-        if (top > v_ref) {  // (warp-uniform) the next power of two above it, within 2^-100 .. 2^127
-          const uint32_t up = min(max((__float_as_uint(top) >> 23) + 1u, 27u), 254u) << 23;
-          const float nref = __uint_as_float(up);
-          const float k = v_ref == 0.f ? 0.f : v_ref / nref;  // (nothing but zeros was added before the first)
-          if (v_ref != 0.f) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        // the next power of two above it, within 2^-100 .. 2^127
+        const uint32_t need = top == 0 ? 0 : min(max((top >> 23) + 1u, 27u), 254u);
+        if (need > v_exp) {  // (the whole warp agrees)
+          if (v_exp != 0) {
+            const float k = exp2_fast((float)((int)v_exp - (int)need));
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[i][e] *= k;
           }
-          v_ref = nref;
+          v_exp = need;
         }
+        // 2^-(v_exp - 127); where every scale so far was zero it does not matter
+        inv_ref = __uint_as_float((v_exp == 254u ? 1u : 254u - max(v_exp, 27u)) << 23);
+        if (v_exp == 254u) inv_ref *= 0.5f;
       }
-      const float inv_ref = TOKEN ? (v_ref > 0.f ? 1.f / v_ref : 0.f) : 1.f;
+      uint32_t pf[STEPS][4], pl[STEPS][4];
+      bool odd = false;  // a new token's V or scale is an infinity or NaN
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        const int k0 = (kg * STEPS + st) * 16;
+      for (int st = 0; st < STEPS; ++st)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           float2 vf = make_float2(1.f, 1.f);
-          if (TOKEN) {
-            vf = *reinterpret_cast<const float2*>(vsc + k0 + nt * 8 + 2 * c);
+          if constexpr (TOKEN) {
+            vf = *reinterpret_cast<const float2*>(vsc + k0 + st * 16 + nt * 8 + 2 * c);
+            if constexpr (SPECIAL) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& y = e ? vf.y : vf.x;
+                const int pos = pos0 + st * 16 + nt * 8 + 2 * c + e;
+                if (pos >= sg.base && !(y < INFINITY)) {
+                  odd |= pos < sg.kv;
+                  y = 0.f;
+                }
+              }
+            }
             vf.x *= inv_ref;
             vf.y *= inv_ref;
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float p0 = exp2_fast(s[st][nt][2 * i] + neg[i]), p1 = exp2_fast(s[st][nt][2 * i + 1] + neg[i]);
+            float p0 = exp2_fast(fmaf(s[st][nt][2 * i], sl2[i], neg[i]));
+            float p1 = exp2_fast(fmaf(s[st][nt][2 * i + 1], sl2[i], neg[i]));
             l[i] += p0 + p1;
-            if (TOKEN) {  // a weight of zero stays zero, whatever the scale holds
-              p0 = p0 == 0.f ? 0.f : p0 * vf.x;
-              p1 = p1 == 0.f ? 0.f : p1 * vf.y;
+            if constexpr (TOKEN) {
+              p0 *= vf.x;
+              p1 *= vf.y;
             }
             const uint32_t u = pack2<E4M3>(p0, p1);
             pf[st][2 * nt + i] = u;
             if (!E4M3) pl[st][2 * nt + i] = pack_rest(p0, p1, u);
           }
         }
-      }
       // ---- O += P V
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
-        const int k0 = (kg * STEPS + st) * 16;
-        const int key = k0 + (((lane >> 3) & 1) << 3) + (lane & 7);
-        const uint32_t rowa = va + key * 128;
-        const uint32_t sw = key & 7, hi = lane >> 4;
-        bool odd_values = false;  // a new token's V holds an infinity or NaN
+        const uint32_t rowa = va + st * (16 * 128);
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) {
+        for (int dt = 0; dt < D / 16; dt += E4M3 ? 2 : 1) {  // (two granules per load)
           uint32_t b[4];
-          if constexpr (!E4M3) {
-            ldsm4_t(b, rowa + (dt / 4) * C::CHUNK + ((((dt & 3) * 2 + hi) ^ sw) << 4));
-          } else {
-            if (dt & 1) continue;
-            ldsm4_t(b, rowa + (((dt + hi) ^ sw) << 4));
-          }
-          if (special) {
-            // slots behind the last token hold anything: they enter as zeros
-            b[0] &= vm[st][0];
-            b[1] &= vm[st][1];
-            b[2] &= vm[st][0];
-            b[3] &= vm[st][1];
-            // so do infinities and NaN of new tokens, which only some rows see (added below)
+          if constexpr (E4M3) ldsm4_t<0>(b, rowa ^ (dt << 4));
+          else if (dt < 4) ldsm4_t<0>(b, rowa ^ ((dt & 3) << 5));
+          else ldsm4_t<C::CHUNK>(b, rowa ^ ((dt & 3) << 5));
+          if constexpr (SPECIAL) {
+            // slots behind the last token hold anything: they enter as zeros; so do the
+            // infinities and NaN of new tokens, which only some rows see (added at the end)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = t * kTile + k0 + (e & 1) * 8 + 2 * c - sg.base;  // of the pair's first key
+              b[e] &= vm[st][e & 1];
+              const int j = pos0 + st * 16 + (e & 1) * 8 + 2 * c - sg.base;  // of the pair's first key
               uint32_t keep = 0xffffffffu;
               if constexpr (!E4M3) {
                 if (j >= 0 && (b[e] & 0x00007f80u) == 0x00007f80u) keep &= 0xffff0000u;
@@ -622,58 +672,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j + 1 >= 0 && (b[e] & 0x007f0000u) == 0x007f0000u) keep &= 0xff00ffffu;
                 if (j + 1 >= 0 && (b[e] & 0x7f000000u) == 0x7f000000u) keep &= 0x00ffffffu;
               }
-              odd_values |= keep != 0xffffffffu;
+              odd |= keep != 0xffffffffu;
               b[e] &= keep;
             }
           }
           if constexpr (!E4M3) {
             mma16816<false>(o[2 * dt], pf[st], b[0], b[1]);
-            mma16816<false>(o[2 * dt], pl[st], b[0], b[1]);
             mma16816<false>(o[2 * dt + 1], pf[st], b[2], b[3]);
+            mma16816<false>(o[2 * dt], pl[st], b[0], b[1]);
             mma16816<false>(o[2 * dt + 1], pl[st], b[2], b[3]);
           } else {
             // bytes (key 2c: d, d + 1), (key 2c + 1: d, d + 1) -> the even d's pair, the odd d's pair
             const uint32_t e0 = __byte_perm(b[0], 0, 0x3120), e1 = __byte_perm(b[1], 0, 0x3120);
             const uint32_t e2 = __byte_perm(b[2], 0, 0x3120), e3 = __byte_perm(b[3], 0, 0x3120);
-            mma16816<true>(o[2 * dt], pf[st], widen_e4m3(e0), widen_e4m3(e1));
-            mma16816<true>(o[2 * dt + 1], pf[st], widen_e4m3(e0 >> 16), widen_e4m3(e1 >> 16));
-            mma16816<true>(o[2 * dt + 2], pf[st], widen_e4m3(e2), widen_e4m3(e3));
-            mma16816<true>(o[2 * dt + 3], pf[st], widen_e4m3(e2 >> 16), widen_e4m3(e3 >> 16));
-          }
-        }
-        if (special && __any_sync(0xffffffffu, odd_values)) {
-          // rare: the infinities and NaN of new tokens, for the rows that see them
-          for (int kk = 0; kk < 16; ++kk) {
-            const int j = t * kTile + k0 + kk - sg.base;
-            if (j < 0 || j >= sg.n) continue;
-            const uint8_t* vrow = ring + vslot * C::SLOT + (k0 + kk) * 128;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (!in[i]) continue;
-              const bool see = a.mask ? (__ldg(a.mask + (long long)(sg.off + tok[i]) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u
-                                      : j <= tok[i];
-              if (!see) continue;
-#pragma unroll
-              for (int q = 0; q < NT; ++q)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  // column of element e of O tile q (see column_of below)
-                  const int d = E4M3 ? (q >> 1) * 16 + 4 * c + 2 * e + (q & 1) : q * 8 + 2 * c + e;
-                  const int gran = d * C::ES / 16;
-                  const uint8_t* p = vrow + (gran >> 3) * C::CHUNK + (((gran & 7) ^ ((k0 + kk) & 7)) << 4) + (d * C::ES & 15);
-                  if constexpr (!E4M3) {
-                    const uint32_t w = *reinterpret_cast<const uint16_t*>(p);
-                    if ((w & 0x7f80u) == 0x7f80u) o[q][2 * i + e] += __uint_as_float(w << 16);
-                  } else if ((*p & 0x7f) == 0x7f) {
-                    o[q][2 * i + e] = __uint_as_float(0x7fc00000u);
-                  }
-                }
-            }
+            mma16816<true>(o[2 * dt], pf[st], widen_lo(e0), widen_lo(e1));
+            mma16816<true>(o[2 * dt + 1], pf[st], widen_hi(e0), widen_hi(e1));
+            mma16816<true>(o[2 * dt + 2], pf[st], widen_lo(e2), widen_lo(e3));
+            mma16816<true>(o[2 * dt + 3], pf[st], widen_hi(e2), widen_hi(e3));
           }
         }
       }
+      if constexpr (SPECIAL) {
+        if (odd) s_odd[segment & 1] = 1;
+      }
+    };
+
+    for (int t = sg.t0; t < sg.t1; ++t) {
+      const int kslot = slot, vslot = slot + 1 == C::SLOTS ? 0 : slot + 1;
+      const uint32_t kphase = phase, vphase = vslot == 0 ? phase ^ 1u : phase;
+      slot = vslot + 1 == C::SLOTS ? 0 : vslot + 1;
+      phase = slot == 0 ? vphase ^ 1u : vphase;
+      if (ok) ok = mbar_wait<true>(full + kslot, kphase, abort_flag, g.status, FP_DEV_TIMEOUT);
+      const float* ksc = reinterpret_cast<const float*>(ring + kslot * C::SLOT + kTileBytes);
+      const float* vsc = reinterpret_cast<const float*>(ring + vslot * C::SLOT + kTileBytes);
+#pragma unroll 1
+      for (int st = 0; st < STEPS_ALL; st += STEPS) {
+        const int k0 = (kg * STEPS_ALL + st) * 16;
+        const uint32_t ka = k_lane + kslot * C::SLOT + st * (16 * 128), va = v_lane + vslot * C::SLOT + st * (16 * 128);
+        if (t * C::TILE + k0 + STEPS * 16 > sg.base)
+          update(std::true_type(), t * C::TILE + k0, k0, ka, va, ksc, vsc, full + vslot, vphase);
+        else
+          update(std::false_type(), t * C::TILE + k0, k0, ka, va, ksc, vsc, full + vslot, vphase);
+      }
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(empty + vslot);
+      if (ok && lane == 0) {
+        mbar_arrive(empty + kslot);
+        mbar_arrive(empty + vslot);
+      }
     }
 
     // ---- the key groups' results meet
@@ -682,12 +727,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (c == 0) {
-        s_m[warp * 16 + gr + 8 * i] = m[i];
+        s_m[warp * 16 + gr + 8 * i] = ref[i];
         s_l[warp * 16 + gr + 8 * i] = l[i];
       }
     }
-    if (TOKEN) v_mul = v_ref;
+    if (TOKEN) v_mul = v_exp == 0 ? 0.f : __uint_as_float(v_exp << 23);
     consumers_sync();
+    if (threadIdx.x == 0) s_odd[(segment + 1) & 1] = 0;  // (its readers have passed the barrier above)
     float big[2], sum[2], w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -698,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum[i] = 0.f;
       // (a group that saw nothing has m = -inf and l = 0; l may be NaN without a maximum)
       for (int k = 0; k < KG; ++k) sum[i] += pl2[k * 16] * (big[i] == -INFINITY ? 1.f : exp2_fast(pm[k * 16] - big[i]));
-      w[i] = big[i] == -INFINITY ? 1.f : exp2_fast(m[i] - big[i]);
+      w[i] = big[i] == -INFINITY ? 1.f : exp2_fast(ref[i] - big[i]);
       w[i] = sum[i] == 0.f ? 0.f : w[i] * v_mul / sum[i];
     }
 #pragma unroll
@@ -733,8 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     consumers_sync();
     const bool whole = sg.whole();
-    const int part = 2 * blockIdx.x + (first_segment ? 0 : 1);
-    first_segment = false;
+    const int part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
+    const bool odd = s_odd[segment & 1] != 0;
     for (int i = threadIdx.x; i < WM * 16 * (D / 4); i += kConsumers) {
       const int lr = i / (D / 4), d4 = i % (D / 4);  // row of the M-tiles, four columns
       const int row = sg.row0 + lr;
@@ -749,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc.z += y.z;
         acc.w += y.w;
       }
+      if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, row / a.G, d4 * 4, C::TILE, acc);
       if (whole) {
         const int t = row / a.G, h = row - t * a.G;
         uint2 pk = make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));
@@ -918,6 +965,7 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   const double scale = t.softmax_scale > 0.f ? (double)t.softmax_scale : 1.0 / std::sqrt((double)g.d);
   a.scale_log2 = (float)(scale * 1.4426950408889634);
   a.grid = sm_count();
+  a.tile = kTileBytes / (g.d * (g.e4m3 ? 1 : 2));
   const size_t rows = (size_t)2 * a.grid * a.rows;
   a.part_o = static_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pad256(rows * g.d * sizeof(float)));
@@ -926,7 +974,7 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   const cuuint64_t es = g.e4m3 ? 1 : 2, P = (cuuint64_t)g.page_size;
   const cuuint64_t dims[4] = {(cuuint64_t)g.d, (cuuint64_t)g.Hkv, P, (cuuint64_t)g.num_pages};
   const cuuint64_t strides[3] = {g.d * es, (cuuint64_t)g.Hkv * g.d * es, P * g.Hkv * g.d * es};
-  const cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1, (cuuint32_t)(g.page_size < kTile ? g.page_size : kTile), 1};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1, (cuuint32_t)(g.page_size < a.tile ? g.page_size : a.tile), 1};
   const CUtensorMapDataType type = g.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   if (!encode_tiled(&mk, type, 4, g.k_pool, dims, strides, box) ||
       !encode_tiled(&mv, type, 4, g.v_pool, dims, strides, box))
