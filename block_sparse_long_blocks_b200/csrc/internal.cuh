@@ -107,10 +107,11 @@ long long attention_units(const Geometry& g);
 cudaError_t launch_unit_order(const Geometry& g, const int32_t* cnt, int* order, int* queue, cudaStream_t s);
 
 // cuTensorMapEncodeTiled (through the runtime's driver entry point) with
-// 128-byte swizzle, 256-byte L2 promotion and zero fill outside the tensor.
+// 128-byte swizzle and zero fill outside the tensor.
 // On failure records the step (fp_last_error) and returns false.
 bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
-                  const cuuint64_t* strides, const cuuint32_t* box);
+                  const cuuint64_t* strides, const cuuint32_t* box,
+                  CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // The status word (FP_DEV_*) of the current device; nullptr on a runtime error.
 unsigned* status_ptr();

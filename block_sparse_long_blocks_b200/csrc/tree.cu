@@ -51,9 +51,20 @@ namespace fp {
 namespace {
 
 constexpr int kWarps = 8;                      // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kThreads = (kWarps + 4) * 32;    // + the producer, alone in a third warpgroup
+// Registers: launched with 168 a thread (three warps per SM sub-partition); the consumers then
+// take 208 and the producer's warpgroup 88: 2 x 128 x 208 + 128 x 88 = 384 x 168.
+constexpr uint32_t kConsumerRegs = 208, kProducerRegs = 88;
+static_assert(2 * 128 * kConsumerRegs + 128 * kProducerRegs <= kThreads * 168, "register split exceeds the launch");
 constexpr int kConsumers = kWarps * 32;
 constexpr int kTileBytes = 32 * 1024;          // of K, and of V
+
+// The reference of a row's exponents rises only when its maximum exceeds it by
+// more than kSlack (log2 units): nearly every step of a short run would raise
+// the exact maximum of one of the rows, and each rise rescales O. f16 weights
+// (e4m3 caches) carry a factor 2^kShift: at most 2^15, and normal down to 2^-22
+// below the reference.
+constexpr float kSlack = 7.f, kShift = 8.f;
 
 struct TreeArgs {
   CacheGeometry g;
@@ -183,6 +194,14 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr), "n"(OFF));
 }
 
+// 16 x 16 bytes per half-warp's addresses, transposed: r[0], r[1] hold (source rows 4c .. 4c + 3) of columns
+// gr and gr + 8 of the first 16 rows, r[2], r[3] those of the second 16
+__device__ __forceinline__ void ldsm2_t8(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
 // c += A (16 x 16, row) * B (16 x 8, col), float32 accumulators
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -197,6 +216,20 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
+}
+// c += A (16 x 32, row) * B (32 x 8, col), e4m3
+__device__ __forceinline__ void mma16832(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two float32 -> two e4m3 codes (the first in the low byte), nearest even, NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_codes(float a, float b) {
+  unsigned short h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+  return h;
 }
 
 // The low or high pair of four e4m3 codes -> two f16 (exact).
@@ -224,7 +257,7 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t u) {
   return pack2<false>(lo - __uint_as_float(u << 16), hi - __uint_as_float(u & 0xffff0000u));
 }
 
-template <bool E4M3, int D>
+template <bool E4M3, int D, int NB>
 struct Cfg {
   static constexpr int ES = E4M3 ? 1 : 2;
   static constexpr int TILE = kTileBytes / (D * ES);     // keys per tile: 128 or 256
@@ -232,9 +265,14 @@ struct Cfg {
   static constexpr int CH_ELEMS = 128 / ES;
   static constexpr int CHUNK = TILE * 128;               // bytes of a tile's chunk
   static constexpr int SLOT = kTileBytes + (E4M3 ? 1024 : 0);  // + the tile's token scales
-  static constexpr int RED = 4 * 16 * D * 4;             // four key groups' O of 16 rows
   static constexpr int SLOTS = 5;
-  static constexpr int SMEM_FIXED = 1024 + SLOTS * SLOT + RED + 2 * kWarps * 16 * 4 + 2 * SLOTS * 8 + 64;
+  static constexpr int ROWS = 8 * NB;
+  static constexpr int QT = E4M3 ? NB : (NB + 1) / 2;    // 16-row A tiles of Q (e4m3: high and low parts)
+  // the warps' O meet in NB rounds of D / NB columns; rows are padded so that the fragments' stores hit 32 banks
+  static constexpr int RED_COLS = D / NB, RED_ROW = RED_COLS + 4;
+  static constexpr int RED = kWarps * ROWS * RED_ROW * 4;
+  static_assert(QT * 16 * D * ES <= RED, "Q lies in the same place while the keys are read");
+  static constexpr int SMEM_FIXED = 1024 + SLOTS * SLOT + RED + (2 * kWarps + 1) * ROWS * 4 + 2 * SLOTS * 8 + 64;
   static_assert(D * ES % 128 == 0, "head dim 128, or 64 with bf16");
   static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
 };
@@ -282,27 +320,30 @@ __device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg
   }
 }
 
-// E4M3: cache type; TOKEN: token scales; WM: M-tiles of 16 rows held by the CTA
-// (8 / WM warps split the keys of each).
-template <bool E4M3, bool TOKEN, int D, int WM>
+// E4M3: cache type; TOKEN: token scales; NB: blocks of 8 rows held by every warp.
+template <bool E4M3, bool TOKEN, int D, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
-  using C = Cfg<E4M3, D>;
-  constexpr int KG = kWarps / WM;        // key groups
-  constexpr int STEPS_ALL = C::TILE / KG / 16;         // 16-key steps per warp and tile,
-  constexpr int STEPS = STEPS_ALL < 2 ? STEPS_ALL : 2;  // of which so many share a softmax update
-  constexpr int NT = D / 8;              // 8-column tiles of O
+  using C = Cfg<E4M3, D, NB>;
+  constexpr int BLOCKS = C::TILE / kWarps / 16;         // 16-key blocks per warp and tile,
+  constexpr int STEPS = NB == 4 || BLOCKS < 2 ? 1 : 2;  // of which so many share a softmax update
+  constexpr int KS = D * C::ES / 32;                    // 32-byte steps of a row
+  constexpr int MT = D / 16;                            // 16-column tiles of O
+  constexpr int QT = C::QT;
+  constexpr bool Q_REGS = NB <= 2;                      // Q's fragments stay in registers
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red = reinterpret_cast<float*>(ring + C::SLOTS * C::SLOT);
-  float* s_m = red + C::RED / 4;               // [warp][16]
-  float* s_l = s_m + kWarps * 16;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_l + kWarps * 16);
+  uint8_t* q_smem = reinterpret_cast<uint8_t*>(red);
+  float* s_m = red + C::RED / 4;               // [warp][row]
+  float* s_l = s_m + kWarps * C::ROWS;
+  float* s_scale = s_l + kWarps * C::ROWS;     // [row]: what a raw score is multiplied by
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + C::ROWS);
   uint64_t* empty = full + C::SLOTS;
   int* misc = reinterpret_cast<int*>(empty + C::SLOTS);
   volatile int* abort_flag = misc;
-  int* warp_sum = misc + 1;                     // [9]
-  volatile int* s_odd = misc + 10;              // [2], by segment parity: see below
+  int* warp_sum = misc + 1;                     // [12]
+  volatile int* s_odd = misc + 13;              // [2], by segment parity: see below
   int* pre = misc + 16;                         // [R + 1]
 
   const CacheGeometry& g = a.g;
@@ -325,7 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (x_first >= total) return;
   const int x_begin = (int)x_first, x_end = min(total, x_begin + share);
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
+    reg_dealloc<kProducerRegs>();
+    if (warp > kWarps) return;
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
       tma_prefetch_desc(&tmK);
@@ -401,17 +444,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------------------------ consumers
-  const int mt = warp / KG, kg = warp % KG;
-  const int gr = lane >> 2, c = lane & 3;  // fragment row and column group
+  reg_alloc<kConsumerRegs>();
+  const int gr = lane >> 2, c = lane & 3;  // fragment row (or column) and column group
+  // Keys of a 16-key block that this thread's scores belong to: fragment column 2c + e of tile 0 and of tile 1.
+  // e4m3: V's transposed load gives a thread four consecutive source rows, two of either tile; tile 1 takes key
+  // 8 + (n ^ 4) as its column n so that eight rows of one load never share a bank, in K or in V.
+  const int key0 = 2 * c, key1 = E4M3 ? 8 + ((2 * c) ^ 4) : 8 + 2 * c;
   // ldmatrix addresses relative to a slot: slots are 1024-aligned, so the
   // 128-byte swizzle of granule 2 i + hi of row `key` is an exclusive or with i << 5
-  uint32_t k_lane, v_lane;
+  uint32_t k_lane, v_lane, q_lane;
   {
-    const int kk = ((lane >> 4) << 3) + (lane & 7), khi = (lane >> 3) & 1;   // K: lanes 16-31 hold keys 8-15
-    const int vk = (((lane >> 3) & 1) << 3) + (lane & 7), vhi = lane >> 4;  // V: lanes 8-15 and 24-31 do
-    k_lane = smem_u32(ring) + (kg * STEPS_ALL * 16 + kk) * 128 + (((khi ^ kk) & 7) << 4);
-    v_lane = smem_u32(ring) + (kg * STEPS_ALL * 16 + vk) * 128 + (((vhi ^ vk) & 7) << 4);
+    const int n = lane & 7, hi = (lane >> 3) & 1;
+    const int kk = lane < 16 ? n : 8 + (E4M3 ? n ^ 4 : n);  // K: lanes 16-31 hold tile 1
+    k_lane = smem_u32(ring) + (warp * BLOCKS * 16 + kk) * 128 + (((hi ^ kk) & 7) << 4);
+    int vk, vg;                                             // V: key, and granule (16 bytes) within a d tile's
+    if (E4M3) {
+      const int i = lane & 15, pair = 2 * (i >> 2) + (i & 1);
+      vk = (i & 2) ? 8 + (pair ^ 4) : pair;
+      vg = STEPS == 1 ? lane >> 4 : 0;                      // lanes 16-31: the next d tile, or the next block's keys
+      if (STEPS == 2) vk += lane & 16;
+    } else {
+      vk = ((lane >> 4) << 3) + n;
+      vg = hi;
+    }
+    v_lane = smem_u32(ring) + (warp * BLOCKS * 16 + vk) * 128 + (((vg ^ vk) & 7) << 4);
+    const int qr = lane & 15, qh = lane >> 4;
+    q_lane = smem_u32(q_smem) + qr * 128 + (((qh ^ qr) & 7) << 4);
   }
+  // fragment `ks` of A tile `qt` of Q
+  auto load_q = [&](uint32_t(&f)[4], int qt, int ks) {
+    ldsm4<0>(f, (q_lane ^ ((ks & 3) << 5)) + (ks >> 2) * (QT * 16 * 128) + qt * (16 * 128));
+  };
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
@@ -421,165 +484,246 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Segment sg = segment_at(a, pre, x, x_end, r);
     x += sg.t1 - sg.t0;
     const int nrows = sg.n * a.G;
-    // ---- this thread's two rows of Q, as A fragments
-    int rho[2], tok[2];
-    bool in[2];
-    uint32_t qf[D / 16][4];
-    float sl2[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      rho[i] = sg.row0 + mt * 16 + gr + 8 * i;
-      in[i] = rho[i] < nrows;
-      const int t = in[i] ? rho[i] / a.G : 0;
-      const int h = in[i] ? rho[i] - t * a.G : 0;
-      tok[i] = t;
-      const __nv_bfloat16* qp = a.q + (long long)(sg.off + t) * a.q_stride + (sg.head * a.G + h) * D;
-      sl2[i] = a.scale_log2;
-      if constexpr (!E4M3) {
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          qf[ks][i] = in[i] ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 2 * c)) : 0u;
-          qf[ks][2 + i] = in[i] ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8 + 2 * c)) : 0u;
+    // ---- Q to shared memory, as the rows of A tiles
+    if constexpr (!E4M3) {
+      for (int i = threadIdx.x; i < QT * 16 * (D / 8); i += kConsumers) {
+        const int row = i / (D / 8), gran = i % (D / 8), rho = sg.row0 + row;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (row < C::ROWS && rho < nrows) {
+          const int t = rho / a.G, h = rho - t * a.G;
+          w = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(sg.off + t) * a.q_stride +
+                                                   (sg.head * a.G + h) * D) + gran);
         }
-      } else {
-        // four consecutive elements per 16: the order in which a thread finds K's bytes
-        uint2 w[D / 16];
-        float mx = 0.f;
+        *reinterpret_cast<uint4*>(q_smem + (gran >> 3) * (QT * 16 * 128) + row * 128 + (((gran ^ row) & 7) << 4)) = w;
+      }
+      if (threadIdx.x < C::ROWS) s_scale[threadIdx.x] = a.scale_log2;
+    } else {
+      constexpr int TPR = 32 / NB, EL = 4 * NB;  // threads per row, elements per thread
+      const int row = threadIdx.x / TPR, part = threadIdx.x % TPR, rho = sg.row0 + row;
+      uint32_t w[EL / 2];
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          w[ks] = in[i] ? __ldg(reinterpret_cast<const uint2*>(qp + ks * 16 + 4 * c)) : make_uint2(0, 0);
-          mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(w[ks].x << 16)), fabsf(__uint_as_float(w[ks].x & 0xffff0000u))),
-                               fmaxf(fabsf(__uint_as_float(w[ks].y << 16)), fabsf(__uint_as_float(w[ks].y & 0xffff0000u)))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // multiply by 2^(14 - floor(log2 max)); rows of zeros, infinities or below 2^-100 take the limits
-        int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127;
-        e = mx == 0.f || e > 127 ? 14 : max(e, -100);
-        const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-        sl2[i] *= __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+      for (int i = 0; i < EL / 2; ++i) w[i] = 0;
+      if (rho < nrows) {
+        const int t = rho / a.G, h = rho - t * a.G;
+        const __nv_bfloat16* qp = a.q + (long long)(sg.off + t) * a.q_stride + (sg.head * a.G + h) * D + part * EL;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          qf[ks][i] = pack2<true>(__uint_as_float(w[ks].x << 16) * up, __uint_as_float(w[ks].x & 0xffff0000u) * up);
-          qf[ks][2 + i] = pack2<true>(__uint_as_float(w[ks].y << 16) * up, __uint_as_float(w[ks].y & 0xffff0000u) * up);
+        for (int i = 0; i < EL / 4; ++i) {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(qp) + i);
+          w[2 * i] = u.x;
+          w[2 * i + 1] = u.y;
         }
       }
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < EL / 2; ++i)
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // times 2^(7 - floor(log2 max)): the largest lies in [2^7, 2^8); rows of zeros or below 2^-100 take the limits
+      const int e = mx == 0.f ? 7 : max((int)((__float_as_uint(mx) >> 23) & 255u) - 127, -100);
+      const float up = mx < INFINITY ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
+      const int hi_row = NB == 1 ? row : (row >> 4) * 32 + (row & 15), lo_row = hi_row + (NB == 1 ? 8 : 16);
+#pragma unroll
+      for (int i = 0; i < EL / 4; ++i) {
+        float v[4] = {__uint_as_float(w[2 * i] << 16) * up, __uint_as_float(w[2 * i] & 0xffff0000u) * up,
+                      __uint_as_float(w[2 * i + 1] << 16) * up, __uint_as_float(w[2 * i + 1] & 0xffff0000u) * up};
+        const uint32_t hi = pack_codes(v[0], v[1]) | (pack_codes(v[2], v[3]) << 16);
+        const uint32_t h01 = widen_lo(hi), h23 = widen_hi(hi);
+        const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+        const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+        const uint32_t lo = pack_codes((v[0] - f01.x) * 32.f, (v[1] - f01.y) * 32.f) |
+                            (pack_codes((v[2] - f23.x) * 32.f, (v[3] - f23.y) * 32.f) << 16);
+        const int at = part * EL + 4 * i, gran = at >> 4;
+        *reinterpret_cast<uint32_t*>(q_smem + hi_row * 128 + (((gran ^ hi_row) & 7) << 4) + (at & 15)) = hi;
+        *reinterpret_cast<uint32_t*>(q_smem + lo_row * 128 + (((gran ^ lo_row) & 7) << 4) + (at & 15)) = lo;
+      }
+      if (part == 0) {
+        float f = a.scale_log2 * __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+        if (!TOKEN) f *= __ldg(g.k_scale + sg.head);
+        if (f == 0.f) f = 1.2e-38f;  // (0 * -inf of a masked key would be NaN)
+        s_scale[row] = f;
+      }
+    }
+    consumers_sync();
+    uint32_t qf[Q_REGS ? QT : 1][Q_REGS ? KS : 1][4];
+    if constexpr (Q_REGS) {
+#pragma unroll
+      for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) load_q(qf[qt][ks], qt, ks);
+    }
+    // this thread's rows of S: gr + 8 b
+    float sl2[NB];
+    int tok[NB];
+    bool in[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int rho = sg.row0 + gr + 8 * b;
+      in[b] = rho < nrows;
+      tok[b] = in[b] ? rho / a.G : 0;
+      sl2[b] = s_scale[gr + 8 * b];
     }
     float v_mul = 1.f;  // what O is multiplied by at the end
-    if (E4M3 && !TOKEN) {
-      const float ks = __ldg(g.k_scale + sg.head);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sl2[i] *= ks;
-        if (sl2[i] == 0.f) sl2[i] = 1.2e-38f;  // (0 * -inf of a masked key would be NaN)
-      }
-      v_mul = __ldg(g.v_scale + sg.head);
-    }
+    if (E4M3 && !TOKEN) v_mul = __ldg(g.v_scale + sg.head);
 
-    float o[NT][4];
+    float o[MT][NB][4];  // columns 16 mt + gr (elements 0, 1) and + 8 (2, 3) of rows 8 b + 2c + {0, 1}
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    // m: running maximum of the unscaled scores; ref = m * sl2 rounded, the exponents' reference
-    float m[2] = {-INFINITY, -INFINITY}, ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][b][e] = 0.f;
+    // ref: the exponents' reference, the scaled maximum at its last rise
+    float ref[NB], l[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      ref[b] = -INFINITY;
+      l[b] = 0.f;
+    }
     uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
 
-    auto row_sees = [&](int i, int j) -> bool {  // row rho[i], new token j
-      return a.mask ? (__ldg(a.mask + (long long)(sg.off + tok[i]) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u
-                    : j <= tok[i];
+    // Which of the 32 positions from base + j0 on (j0 > -32) row gr + 8 b sees, as bits.
+    auto row_sees = [&](int b, int j0) -> uint32_t {
+      const uint32_t cached = j0 < 0 ? (1u << -j0) - 1u : 0u;
+      if (!in[b]) return cached;
+      uint32_t bits;
+      if (a.mask) {
+        const uint32_t* words = a.mask + (long long)(sg.off + tok[b]) * a.mask_words;
+        auto word = [&](int i) -> uint32_t { return i >= 0 && i * 32 < sg.n ? __ldg(words + i) : 0u; };
+        const int i = j0 >> 5;  // (-1 for negative j0)
+        bits = __funnelshift_r(word(i), word(i + 1), j0 & 31);
+      } else {
+        const int seen = tok[b] + 1 - j0;  // (j0 + bit <= tok)
+        bits = seen >= 32 ? 0xffffffffu : seen > 0 ? (1u << seen) - 1u : 0u;
+      }
+      return bits | cached;
     };
 
-    // STEPS steps of 16 keys of one tile: first position pos0, first key k0 of the
+    // STEPS blocks of 16 keys of one tile: first position pos0, first key k0 of the
     // tile; SPECIAL: some are new tokens, or slots behind the last one.
     auto update = [&](auto special, int pos0, int k0, uint32_t ka, uint32_t va, const float* ksc, const float* vsc,
                       uint64_t* vfull, uint32_t vphase) {
       constexpr bool SPECIAL = decltype(special)::value;
-      float s[STEPS][2][4];
+      float s[STEPS][NB][2][2];
+      {
+        float acc[STEPS][2][QT][4];
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
+        for (int st = 0; st < STEPS; ++st)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[st][0][e] = s[st][1][e] = 0.f;
-        const uint32_t rowa = ka + st * (16 * 128);
-        if constexpr (!E4M3) {
+          for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t b[4];
-            if (ks < 4) ldsm4<0>(b, rowa ^ ((ks & 3) << 5));
-            else ldsm4<C::CHUNK>(b, rowa ^ ((ks & 3) << 5));
-            mma16816<false>(s[st][0], qf[ks], b[0], b[1]);
-            mma16816<false>(s[st][1], qf[ks], b[2], b[3]);
+            for (int e = 0; e < 4; ++e) acc[st][0][qt][e] = acc[st][1][qt][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t kb[STEPS][4];  // (tile 0, first and second 16 bytes), (tile 1, the same)
+#pragma unroll
+          for (int st = 0; st < STEPS; ++st) {
+            const uint32_t rowa = (ka + st * (16 * 128)) ^ ((ks & 3) << 5);
+            if (ks < 4) ldsm4<0>(kb[st], rowa);
+            else ldsm4<C::CHUNK>(kb[st], rowa);
           }
-        } else {
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            uint32_t b[4];  // (keys 0-7, granules 2kk and 2kk + 1), (keys 8-15, the same)
-            ldsm4<0>(b, rowa ^ (kk << 5));
-            mma16816<true>(s[st][0], qf[2 * kk], widen_lo(b[0]), widen_hi(b[0]));
-            mma16816<true>(s[st][1], qf[2 * kk], widen_lo(b[2]), widen_hi(b[2]));
-            mma16816<true>(s[st][0], qf[2 * kk + 1], widen_lo(b[1]), widen_hi(b[1]));
-            mma16816<true>(s[st][1], qf[2 * kk + 1], widen_lo(b[3]), widen_hi(b[3]));
+          for (int qt = 0; qt < QT; ++qt) {
+            uint32_t tmp[4];
+            if constexpr (!Q_REGS) load_q(tmp, qt, ks);
+            const uint32_t(&qa)[4] = Q_REGS ? qf[Q_REGS ? qt : 0][Q_REGS ? ks : 0] : tmp;
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                if constexpr (E4M3) mma16832(acc[st][nt][qt], qa, kb[st][2 * nt], kb[st][2 * nt + 1]);
+                else mma16816<false>(acc[st][nt][qt], qa, kb[st][2 * nt], kb[st][2 * nt + 1]);
+              }
           }
         }
-      }
-      // this thread's keys are 16 st + 8 nt + 2c + {0, 1} (elements 0, 1: row gr; 2, 3: row gr + 8)
-      uint32_t vm[STEPS][2];  // V rows that enter the product, as masks of key pairs
-      float mx[2] = {m[0], m[1]};
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st)
+        for (int st = 0; st < STEPS; ++st)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if constexpr (!E4M3) s[st][b][nt][e] = acc[st][nt][b >> 1][(b & 1) * 2 + e];
+                else if constexpr (NB == 1) s[st][b][nt][e] = fmaf(acc[st][nt][0][2 + e], 0x1p-5f, acc[st][nt][0][e]);
+                else
+                  s[st][b][nt][e] = fmaf(acc[st][nt][(b & ~1) + 1][(b & 1) * 2 + e], 0x1p-5f,
+                                         acc[st][nt][b & ~1][(b & 1) * 2 + e]);
+              }
+      }
+      // V rows that enter the product: masks of this thread's keys (e4m3: four bytes; bf16: two halves of two words),
+      // and which of them are new tokens
+      uint32_t vkeep[STEPS][E4M3 ? 1 : 2], vnew[STEPS][E4M3 ? 1 : 2];
+      float mx[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) mx[b] = -INFINITY;
+      uint32_t see[SPECIAL ? NB : 1];
+      if constexpr (SPECIAL) {
+        const int there = sg.kv - pos0;  // positions behind the last token
+        const uint32_t some = there >= 32 ? 0xffffffffu : there > 0 ? (1u << there) - 1u : 0u;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) see[b] = row_sees(b, pos0 - sg.base) & some;
+      }
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        if constexpr (SPECIAL) vkeep[st][0] = vnew[st][0] = vkeep[st][E4M3 ? 0 : 1] = vnew[st][E4M3 ? 0 : 1] = 0u;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
+          const int key = st * 16 + (nt ? key1 : key0);
           if constexpr (TOKEN) {
-            const float2 kf = *reinterpret_cast<const float2*>(ksc + k0 + st * 16 + nt * 8 + 2 * c);
+            const float2 kf = *reinterpret_cast<const float2*>(ksc + k0 + key);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[st][nt][e] *= (e & 1) ? kf.y : kf.x;
+            for (int b = 0; b < NB; ++b) {
+              s[st][b][nt][0] *= kf.x;
+              s[st][b][nt][1] *= kf.y;
+            }
           }
           if constexpr (SPECIAL) {
-            vm[st][nt] = 0xffffffffu;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int pos = pos0 + st * 16 + nt * 8 + 2 * c + e;
-              const int j = pos - sg.base;
-              if (pos >= sg.kv) vm[st][nt] &= e ? 0x0000ffffu : 0xffff0000u;
+              const int pos = pos0 + key + e;
+              const uint32_t bits = E4M3 ? 0xffu << (16 * nt + 8 * e) : 0xffffu << (16 * e);
+              if (pos < sg.kv) vkeep[st][E4M3 ? 0 : nt] |= bits;
+              if (pos >= sg.base) vnew[st][E4M3 ? 0 : nt] |= bits;
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                bool see = j < 0;
-                if (j >= 0 && j < sg.n && in[i]) see = row_sees(i, j);
-                if (!see) s[st][nt][2 * i + e] = -INFINITY;
-              }
+              for (int b = 0; b < NB; ++b)
+                if (!(see[b] >> (key + e) & 1u)) s[st][b][nt][e] = -INFINITY;
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[st][nt][e]);
+          for (int b = 0; b < NB; ++b) mx[b] = fmaxf(mx[b], fmaxf(s[st][b][nt][0], s[st][b][nt][1]));
         }
+      }
 
       // ---- softmax
+      bool grew = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+      for (int b = 0; b < NB; ++b) {
+        mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 1));
+        mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 2)) * sl2[b];
+        grew |= mx[b] > ref[b] + kSlack;
       }
-      if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-        float f[2];
+      if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float nref = mx[i] * sl2[i];
-          f[i] = mx[i] > m[i] ? exp2_fast(ref[i] - nref) : 1.f;
-          if (mx[i] > m[i]) {
-            m[i] = mx[i];
-            ref[i] = nref;
+        for (int b = 0; b < NB; ++b) {
+          float f = 1.f;
+          if (mx[b] > ref[b] + kSlack) {
+            f = exp2_fast(ref[b] - mx[b]);
+            ref[b] = mx[b];
           }
-          l[i] *= f[i];
+          l[b] *= f;
+          // O's columns are rows 2c and 2c + 1 of the block
+          const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][b][e] *= (e & 1) ? f1 : f0;
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= f[e >> 1];
       }
-      // weights relative to the running maximum; f16 ones to 2^14 above it
-      float neg[2];
+      // weights relative to the reference; f16 ones times 2^kShift
+      float neg[NB];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) neg[i] = ref[i] == -INFINITY ? 0.f : (E4M3 ? 14.f - ref[i] : -ref[i]);
+      for (int b = 0; b < NB; ++b) neg[b] = ref[b] == -INFINITY ? 0.f : (E4M3 ? kShift - ref[b] : -ref[b]);
 
       if (ok) ok = mbar_wait<true>(vfull, vphase, abort_flag, g.status, FP_DEV_TIMEOUT);
       float inv_ref = 1.f;
@@ -598,9 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (v_exp != 0) {
             const float k = exp2_fast((float)((int)v_exp - (int)need));
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[i][e] *= k;
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][b][e] *= k;
           }
           v_exp = need;
         }
@@ -608,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         inv_ref = __uint_as_float((v_exp == 254u ? 1u : 254u - max(v_exp, 27u)) << 23);
         if (v_exp == 254u) inv_ref *= 0.5f;
       }
-      uint32_t pf[STEPS][4], pl[STEPS][4];
+      uint32_t pf[STEPS][NB][2], pl[STEPS][NB][2];
       bool odd = false;  // a new token's V or scale is an infinity or NaN
 #pragma unroll
       for (int st = 0; st < STEPS; ++st)
@@ -616,12 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nt = 0; nt < 2; ++nt) {
           float2 vf = make_float2(1.f, 1.f);
           if constexpr (TOKEN) {
-            vf = *reinterpret_cast<const float2*>(vsc + k0 + st * 16 + nt * 8 + 2 * c);
+            const int key = st * 16 + (nt ? key1 : key0);
+            vf = *reinterpret_cast<const float2*>(vsc + k0 + key);
             if constexpr (SPECIAL) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float& y = e ? vf.y : vf.x;
-                const int pos = pos0 + st * 16 + nt * 8 + 2 * c + e;
+                const int pos = pos0 + key + e;
                 if (pos >= sg.base && !(y < INFINITY)) {
                   odd |= pos < sg.kv;
                   y = 0.f;
@@ -632,63 +779,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             vf.y *= inv_ref;
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float p0 = exp2_fast(fmaf(s[st][nt][2 * i], sl2[i], neg[i]));
-            float p1 = exp2_fast(fmaf(s[st][nt][2 * i + 1], sl2[i], neg[i]));
-            l[i] += p0 + p1;
+          for (int b = 0; b < NB; ++b) {
+            float p0 = exp2_fast(fmaf(s[st][b][nt][0], sl2[b], neg[b]));
+            float p1 = exp2_fast(fmaf(s[st][b][nt][1], sl2[b], neg[b]));
+            l[b] += p0 + p1;
             if constexpr (TOKEN) {
               p0 *= vf.x;
               p1 *= vf.y;
             }
             const uint32_t u = pack2<E4M3>(p0, p1);
-            pf[st][2 * nt + i] = u;
-            if (!E4M3) pl[st][2 * nt + i] = pack_rest(p0, p1, u);
+            pf[st][b][nt] = u;
+            if (!E4M3) pl[st][b][nt] = pack_rest(p0, p1, u);
           }
         }
-      // ---- O += P V
+      // ---- O^T += V^T P^T
+      // slots behind the last token hold anything: they enter as zeros; so do the
+      // infinities and NaN of new tokens, which only some rows see (added at the end)
+      auto clean = [&](uint32_t& w, int st, int half) {
+        if constexpr (SPECIAL) {
+          const uint32_t magic = E4M3 ? 0x7f7f7f7fu : 0x7f807f80u;
+          w &= vkeep[st][half];
+          const uint32_t bad = (E4M3 ? __vcmpeq4(w & magic, magic) : __vcmpeq2(w & magic, magic)) & vnew[st][half];
+          odd |= bad != 0;
+          w &= ~bad;
+        }
+      };
+      if constexpr (!E4M3) {
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        const uint32_t rowa = va + st * (16 * 128);
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int dt = 0; dt < D / 16; dt += E4M3 ? 2 : 1) {  // (two granules per load)
-          uint32_t b[4];
-          if constexpr (E4M3) ldsm4_t<0>(b, rowa ^ (dt << 4));
-          else if (dt < 4) ldsm4_t<0>(b, rowa ^ ((dt & 3) << 5));
-          else ldsm4_t<C::CHUNK>(b, rowa ^ ((dt & 3) << 5));
-          if constexpr (SPECIAL) {
-            // slots behind the last token hold anything: they enter as zeros; so do the
-            // infinities and NaN of new tokens, which only some rows see (added at the end)
+          for (int st = 0; st < STEPS; ++st) {
+            uint32_t w[4];
+            const uint32_t rowa = (va + st * (16 * 128)) ^ ((mt & 3) << 5);
+            if (mt < 4) ldsm4_t<0>(w, rowa);
+            else ldsm4_t<C::CHUNK>(w, rowa);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              b[e] &= vm[st][e & 1];
-              const int j = pos0 + st * 16 + (e & 1) * 8 + 2 * c - sg.base;  // of the pair's first key
-              uint32_t keep = 0xffffffffu;
-              if constexpr (!E4M3) {
-                if (j >= 0 && (b[e] & 0x00007f80u) == 0x00007f80u) keep &= 0xffff0000u;
-                if (j + 1 >= 0 && (b[e] & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
-              } else {
-                if (j >= 0 && (b[e] & 0x0000007fu) == 0x0000007fu) keep &= 0xffffff00u;
-                if (j >= 0 && (b[e] & 0x00007f00u) == 0x00007f00u) keep &= 0xffff00ffu;
-                if (j + 1 >= 0 && (b[e] & 0x007f0000u) == 0x007f0000u) keep &= 0xff00ffffu;
-                if (j + 1 >= 0 && (b[e] & 0x7f000000u) == 0x7f000000u) keep &= 0x00ffffffu;
-              }
-              odd |= keep != 0xffffffffu;
-              b[e] &= keep;
+            for (int e = 0; e < 4; ++e) clean(w[e], st, e >> 1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              mma16816<false>(o[mt][b], w, pf[st][b][0], pf[st][b][1]);
+              mma16816<false>(o[mt][b], w, pl[st][b][0], pl[st][b][1]);
             }
           }
-          if constexpr (!E4M3) {
-            mma16816<false>(o[2 * dt], pf[st], b[0], b[1]);
-            mma16816<false>(o[2 * dt + 1], pf[st], b[2], b[3]);
-            mma16816<false>(o[2 * dt], pl[st], b[0], b[1]);
-            mma16816<false>(o[2 * dt + 1], pl[st], b[2], b[3]);
-          } else {
-            // bytes (key 2c: d, d + 1), (key 2c + 1: d, d + 1) -> the even d's pair, the odd d's pair
-            const uint32_t e0 = __byte_perm(b[0], 0, 0x3120), e1 = __byte_perm(b[1], 0, 0x3120);
-            const uint32_t e2 = __byte_perm(b[2], 0, 0x3120), e3 = __byte_perm(b[3], 0, 0x3120);
-            mma16816<true>(o[2 * dt], pf[st], widen_lo(e0), widen_lo(e1));
-            mma16816<true>(o[2 * dt + 1], pf[st], widen_hi(e0), widen_hi(e1));
-            mma16816<true>(o[2 * dt + 2], pf[st], widen_lo(e2), widen_lo(e3));
-            mma16816<true>(o[2 * dt + 3], pf[st], widen_hi(e2), widen_hi(e3));
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < MT; mt += STEPS == 1 ? 2 : 1) {
+          uint32_t w[4];
+          ldsm2_t8(w, va ^ (mt << 4));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {  // the load's halves: another d tile, or another block of keys
+            const int st = STEPS == 1 ? 0 : i, tile = STEPS == 1 ? mt + i : mt;
+            clean(w[2 * i], st, 0);
+            clean(w[2 * i + 1], st, 0);
+            const uint32_t f[4] = {widen_lo(w[2 * i]), widen_lo(w[2 * i + 1]), widen_hi(w[2 * i]),
+                                   widen_hi(w[2 * i + 1])};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16816<true>(o[tile][b], f, pf[st][b][0], pf[st][b][1]);
           }
         }
       }
@@ -706,8 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* ksc = reinterpret_cast<const float*>(ring + kslot * C::SLOT + kTileBytes);
       const float* vsc = reinterpret_cast<const float*>(ring + vslot * C::SLOT + kTileBytes);
 #pragma unroll 1
-      for (int st = 0; st < STEPS_ALL; st += STEPS) {
-        const int k0 = (kg * STEPS_ALL + st) * 16;
+      for (int st = 0; st < BLOCKS; st += STEPS) {
+        const int k0 = (warp * BLOCKS + st) * 16;
         const uint32_t ka = k_lane + kslot * C::SLOT + st * (16 * 128), va = v_lane + vslot * C::SLOT + st * (16 * 128);
         if (t * C::TILE + k0 + STEPS * 16 > sg.base)
           update(std::true_type(), t * C::TILE + k0, k0, ka, va, ksc, vsc, full + vslot, vphase);
@@ -721,103 +867,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    // ---- the key groups' results meet
+    // ---- the warps' results meet
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    for (int b = 0; b < NB; ++b) {
+      l[b] += __shfl_xor_sync(0xffffffffu, l[b], 1);
+      l[b] += __shfl_xor_sync(0xffffffffu, l[b], 2);
       if (c == 0) {
-        s_m[warp * 16 + gr + 8 * i] = ref[i];
-        s_l[warp * 16 + gr + 8 * i] = l[i];
+        s_m[warp * C::ROWS + gr + 8 * b] = ref[b];
+        s_l[warp * C::ROWS + gr + 8 * b] = l[b];
       }
     }
     if (TOKEN) v_mul = v_exp == 0 ? 0.f : __uint_as_float(v_exp << 23);
     consumers_sync();
     if (threadIdx.x == 0) s_odd[(segment + 1) & 1] = 0;  // (its readers have passed the barrier above)
-    float big[2], sum[2], w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* pm = s_m + mt * KG * 16 + gr + 8 * i;
-      const float* pl2 = s_l + mt * KG * 16 + gr + 8 * i;
-      big[i] = -INFINITY;
-      for (int k = 0; k < KG; ++k) big[i] = fmaxf(big[i], pm[k * 16]);
-      sum[i] = 0.f;
-      // (a group that saw nothing has m = -inf and l = 0; l may be NaN without a maximum)
-      for (int k = 0; k < KG; ++k) sum[i] += pl2[k * 16] * (big[i] == -INFINITY ? 1.f : exp2_fast(pm[k * 16] - big[i]));
-      w[i] = big[i] == -INFINITY ? 1.f : exp2_fast(ref[i] - big[i]);
-      w[i] = sum[i] == 0.f ? 0.f : w[i] * v_mul / sum[i];
-    }
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[q][e] = w[e >> 1] == 0.f ? 0.f : o[q][e] * w[e >> 1];
-    // sum over the key groups: the upper half adds to the lower through `red`, then all threads add what is left
-    constexpr int HALF = kWarps / 2;
-    auto red_at = [&](int buf, int q, int i, int e) -> float* {
-      const int d = E4M3 ? (q >> 1) * 16 + 4 * c + 2 * e + (q & 1) : q * 8 + 2 * c + e;
-      return red + (buf * 16 + gr + 8 * i) * D + d;
-    };
-    // pairs (mt, kg) and (mt, kg + KG / 2) share a buffer
-    const bool upper = kg >= KG / 2;
-    const int buf = mt * (KG / 2) + (upper ? kg - KG / 2 : kg);
-    static_assert(WM * (KG / 2) == HALF, "four buffers");
-    if (upper) {
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *red_at(buf, q, e >> 1, e & 1) = o[q][e];
-    }
-    consumers_sync();
-    if (!upper) {
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float* p = red_at(buf, q, e >> 1, e & 1);
-          *p += o[q][e];
-        }
-    }
-    consumers_sync();
     const bool whole = sg.whole();
     const int part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
-    const bool odd = s_odd[segment & 1] != 0;
-    for (int i = threadIdx.x; i < WM * 16 * (D / 4); i += kConsumers) {
-      const int lr = i / (D / 4), d4 = i % (D / 4);  // row of the M-tiles, four columns
-      const int row = sg.row0 + lr;
-      if (row >= nrows) continue;
-      const float* src = red + (((lr >> 4) * (KG / 2)) * 16 + (lr & 15)) * D + d4 * 4;
-      float4 acc = *reinterpret_cast<const float4*>(src);
 #pragma unroll
-      for (int k = 1; k < KG / 2; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(src + k * 16 * D);
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
-      }
-      if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, row / a.G, d4 * 4, C::TILE, acc);
-      if (whole) {
-        const int t = row / a.G, h = row - t * a.G;
-        uint2 pk = make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));
-        *reinterpret_cast<uint2*>(a.o + ((long long)(sg.off + t) * a.Hq + sg.head * a.G + h) * D + d4 * 4) = pk;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + ((long long)part * a.rows + lr) * D + d4 * 4) = acc;
-      }
-    }
-    if (kg == 0 && c == 0) {
+    for (int b = 0; b < NB; ++b) {
+      const float* pm = s_m + gr + 8 * b;
+      const float* pl2 = s_l + gr + 8 * b;
+      float big = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (!in[i]) continue;
-        // the weights' 2^14 (e4m3) comes off the logarithm
-        const float lse2 = sum[i] == 0.f ? -INFINITY
-                                         : (big[i] == -INFINITY ? 0.f : big[i]) + log2f(sum[i]) - (E4M3 ? 14.f : 0.f);
+      for (int k = 0; k < kWarps; ++k) big = fmaxf(big, pm[k * C::ROWS]);
+      // (a warp that saw nothing has ref = -inf and l = 0; l may be NaN without a maximum)
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        sum += pl2[k * C::ROWS] * (big == -INFINITY ? 1.f : exp2_fast(pm[k * C::ROWS] - big));
+      float w = big == -INFINITY ? 1.f : exp2_fast(ref[b] - big);
+      w = sum == 0.f ? 0.f : w * v_mul / sum;
+      const float w0 = __shfl_sync(0xffffffffu, w, 8 * c), w1 = __shfl_sync(0xffffffffu, w, 8 * c + 4);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float we = (e & 1) ? w1 : w0;
+          o[i][b][e] = we == 0.f ? 0.f : o[i][b][e] * we;
+        }
+      if (warp == 0 && c == 0 && in[b]) {
+        // the weights' factor (e4m3) comes off the logarithm
+        const float lse2 = sum == 0.f ? -INFINITY : (big == -INFINITY ? 0.f : big) + log2f(sum) - (E4M3 ? kShift : 0.f);
         if (!whole) {
-          a.part_lse[(long long)part * a.rows + mt * 16 + gr + 8 * i] = lse2;
+          a.part_lse[(long long)part * a.rows + gr + 8 * b] = lse2;
         } else if (a.lse) {
-          const int h = rho[i] - tok[i] * a.G;
-          a.lse[(long long)(sg.head * a.G + h) * g.total_tokens + sg.off + tok[i]] = lse2 * 0.69314718055994531f;
+          const int h = sg.row0 + gr + 8 * b - tok[b] * a.G;
+          a.lse[(long long)(sg.head * a.G + h) * g.total_tokens + sg.off + tok[b]] = lse2 * 0.69314718055994531f;
         }
       }
+    }
+    const bool odd = s_odd[segment & 1] != 0;
+#pragma unroll
+    for (int round = 0; round < NB; ++round) {
+#pragma unroll
+      for (int i = 0; i < MT / NB; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            red[(warp * C::ROWS + 8 * b + 2 * c + (e & 1)) * C::RED_ROW + i * 16 + gr + (e >> 1) * 8] =
+                o[round * (MT / NB) + i][b][e];
+      consumers_sync();
+      constexpr int VECS = C::RED_COLS / 4;
+      const int lr = threadIdx.x / VECS, col = threadIdx.x % VECS * 4;
+      const int row = sg.row0 + lr;
+      if (lr < C::ROWS && row < nrows) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float4 y = *reinterpret_cast<const float4*>(red + (k * C::ROWS + lr) * C::RED_ROW + col);
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+        }
+        const int d = round * C::RED_COLS + col;
+        const int t = row / a.G, h = row - t * a.G;
+        if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, t, d, C::TILE, acc);
+        if (whole) {
+          *reinterpret_cast<uint2*>(a.o + ((long long)(sg.off + t) * a.Hq + sg.head * a.G + h) * D + d) =
+              make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((long long)part * a.rows + lr) * D + d) = acc;
+        }
+      }
+      consumers_sync();  // the next round, or the next segment's Q, may be written
     }
   }
 }
@@ -909,12 +1041,12 @@ int sm_count() {
   return n;
 }
 
-int unit_rows(int max_rows) { return max_rows <= 16 ? 16 : 32; }
+int unit_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 32; }
 
-template <bool E4M3, bool TOKEN, int D, int WM>
+template <bool E4M3, bool TOKEN, int D, int NB>
 cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  using C = Cfg<E4M3, D>;
-  auto kern = tree_kernel<E4M3, TOKEN, D, WM>;
+  using C = Cfg<E4M3, D, NB>;
+  auto kern = tree_kernel<E4M3, TOKEN, D, NB>;
   const int smem = C::SMEM_FIXED + (a.g.R + 1) * 4;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -935,7 +1067,9 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
 
 template <bool E4M3, bool TOKEN, int D>
 cudaError_t run_rows(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  return a.rows == 16 ? run<E4M3, TOKEN, D, 1>(a, mk, mv, s) : run<E4M3, TOKEN, D, 2>(a, mk, mv, s);
+  if (a.rows == 8) return run<E4M3, TOKEN, D, 1>(a, mk, mv, s);
+  if (a.rows == 16) return run<E4M3, TOKEN, D, 2>(a, mk, mv, s);
+  return run<E4M3, TOKEN, D, 4>(a, mk, mv, s);
 }
 
 size_t pad256(size_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -976,8 +1110,9 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   const cuuint64_t strides[3] = {g.d * es, (cuuint64_t)g.Hkv * g.d * es, P * g.Hkv * g.d * es};
   const cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1, (cuuint32_t)(g.page_size < a.tile ? g.page_size : a.tile), 1};
   const CUtensorMapDataType type = g.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!encode_tiled(&mk, type, 4, g.k_pool, dims, strides, box) ||
-      !encode_tiled(&mv, type, 4, g.v_pool, dims, strides, box))
+  const auto promotion = g.d * es == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  if (!encode_tiled(&mk, type, 4, g.k_pool, dims, strides, box, promotion) ||
+      !encode_tiled(&mv, type, 4, g.v_pool, dims, strides, box, promotion))
     return FP_ERR_CUDA;
   cudaError_t e;
   if (g.e4m3) e = g.token_scale ? run_rows<true, true, 128>(a, mk, mv, s) : run_rows<true, false, 128>(a, mk, mv, s);
