@@ -7,30 +7,37 @@
 //   m = max_j x, p = 2^(x - m), l = sum p, O = sum p v / l, lse = (m + log2 l) ln 2
 // Online over the keys: when m grows, l and O are multiplied by 2^(m_old - m).
 //
-// What bounds it: every cached row is read once per M-tile of 16 or 32 rows,
-// 4 * rows flops per element, so up to ~250 rows (bf16) HBM is the floor. The
-// keys of ALL requests, KV heads and M-tiles form one axis of tiles (32 KB of K:
-// 128 keys of 256 bytes, or 256 of 128), cut evenly over one persistent CTA per SM, however ragged the lengths. A unit
-// (request, KV head, M-tile) that lies within one CTA's share is finished there;
-// the others leave normalised partial rows (float32 O, base-2 lse) in the
-// workspace, at most two per CTA, which a second kernel (a programmatic
-// dependent launch) combines in a fixed order: O = sum_i 2^(lse_i - lse) O_i.
+// What bounds it: every cached row is read once per unit, 4 * rows flops per
+// element, so up to ~250 rows (bf16) HBM is the floor. The keys of ALL requests,
+// KV heads and units form one axis of tiles (32 KB of K: 128 keys of 256 bytes,
+// or 256 of 128), cut evenly over one persistent CTA per SM, however ragged the
+// lengths. A unit (request, KV head, rows) that lies within one CTA's share is
+// finished there; the others leave normalised partial rows (float32 O, base-2
+// lse) in the workspace, at most two per CTA, which a second kernel (a
+// programmatic dependent launch) combines in a fixed order:
+// O = sum_i 2^(lse_i - lse) O_i.
+// This file: units of 8 or 16 rows, single tokens and small trees. More rows go
+// to tree_wide.cu, where tcgen05 multiplies M-tiles of 128.
 //
 // A CTA: warp 8 issues TMA copies of K and V tiles (4-D boxes per page, 128-byte
-// swizzle, and the tile's token scales) into a ring of five 32 KB slots; warps 0-7 hold the M-tiles' rows as mma.sync fragments (16 rows
-// per warp) and split the tile's keys, so no warp waits for another until the
-// unit's end, where the key groups' (m, l, O) meet in shared memory.
+// swizzle, and the tile's token scales) into a ring of five 32 KB slots; warps
+// 0-7 all hold the unit's rows and split the tile's keys, so no warp waits for
+// another until the unit's end, where their (m, l, O) meet in shared memory.
 // mma.sync and not tcgen05 here: 8 or 16 useful rows would fill a sixteenth or
-// an eighth of a 128-row tcgen05 tile, and the softmax would run in as many
-// threads; at these row counts HBM is the limit and the legacy pipe is ~20 % busy.
+// an eighth of a 128-row tcgen05 tile. S = Q K^T has the rows as M (16); the
+// second product is transposed, O^T = V^T P^T, so that 8 rows are its whole N
+// and the weights go from accumulators to operands within their thread.
 //
 // Operands: bf16 caches multiply bf16 q and k exactly, and p as bf16 hi + lo
-// (two products: the weights keep 16 bits; the tensor pipe has room). e4m3 caches
-// widen k and v exactly to f16; q goes to f16 as q * 2^e with e per row such that
-// max |q| lies in [2^14, 2^15): exact for every element within 2^-29 of the
-// largest. p carries a factor 2^14 (f16's normal range then reaches 2^-28 below
-// the running maximum). Token scales of V multiply p, divided by a running power
-// of two >= the largest v_scale so far, so p stays within f16.
+// (two products: the weights keep 16 bits; the tensor pipe has room). e4m3
+// caches: S on the e4m3 path (mma.m16n8k32 runs at 4.4 clocks a warp, half the
+// f16 instruction's for twice the keys, and needs no widening; its sums were
+// measured exact to 2^-22 of sum |q k|), with q * 2^e (e per row such that max |q|
+// lies in [2^7, 2^8)) as hi + 2^-5 lo, two e4m3 values whose sum is q exactly for
+// every element within 2^-15 of the largest; up to 8 rows both fill one M tile.
+// V is widened exactly to f16; p carries a factor 2^kShift into f16's normal
+// range. Token scales of V multiply p, divided by a running power of two >= the
+// largest v_scale so far, so p stays within f16.
 // Every wait is bounded; after one ran out the consumers go on without waiting
 // (their loops have fixed lengths, so they still meet at every barrier) and
 // release no slot any more: its copy may be in flight. The producer stops and
@@ -43,10 +50,11 @@
 #include <cmath>
 #include <type_traits>
 
-#include "internal.cuh"
-#include "sm100.cuh"
+#include "tree.cuh"
 
 namespace fp {
+
+using namespace tree;
 
 namespace {
 
@@ -59,128 +67,9 @@ static_assert(2 * 128 * kConsumerRegs + 128 * kProducerRegs <= kThreads * 168, "
 constexpr int kConsumers = kWarps * 32;
 constexpr int kTileBytes = 32 * 1024;          // of K, and of V
 
-// The reference of a row's exponents rises only when its maximum exceeds it by
-// more than kSlack (log2 units): nearly every step of a short run would raise
-// the exact maximum of one of the rows, and each rise rescales O. f16 weights
-// (e4m3 caches) carry a factor 2^kShift: at most 2^15, and normal down to 2^-22
-// below the reference.
-constexpr float kSlack = 7.f, kShift = 8.f;
-
-struct TreeArgs {
-  CacheGeometry g;
-  int Hq, G;
-  int max_tokens;
-  int rows;               // rows per M-tile unit
-  int tile;               // keys per tile
-  const uint32_t* mask;
-  int mask_words;
-  const __nv_bfloat16* q;
-  long long q_stride;
-  __nv_bfloat16* o;
-  float* lse;
-  float scale_log2;
-  float* part_o;          // [2 * grid][rows][d]
-  float* part_lse;        // [2 * grid][rows], base 2
-  int grid;
-};
-
-// ---------------------------------------------------------------------------
-// the axis of tiles
-// ---------------------------------------------------------------------------
-// Tiles of the keys of request r, and M-tile units per KV head (0 for a request
-// that is empty, or rejected).
-__device__ __forceinline__ void request_tiles(const TreeArgs& a, int r, int& off, int& n, int& kv, int& nt, int& nm) {
-  nt = nm = 0;
-  if (!cache_span(a.g, r, off, n, kv)) return;
-  if (n > a.max_tokens) {
-    atomicOr(a.g.status, FP_DEV_BAD_SEQLENS);
-    n = 0;
-  }
-  if (n == 0) return;
-  nt = (kv + a.tile - 1) / a.tile;
-  nm = (n * a.G + a.rows - 1) / a.rows;
-}
-
-// Exclusive prefix of the requests' tile counts into pre[0 .. R] (all threads of
-// the block; `warp_sum` has one int per warp). The host bounds the total by INT_MAX.
-__device__ __forceinline__ void prefix_tiles(const TreeArgs& a, int* pre, int* warp_sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int carry = 0;
-  for (int r0 = 0; r0 < a.g.R; r0 += blockDim.x) {
-    const int r = r0 + threadIdx.x;
-    int mine = 0;
-    if (r < a.g.R) {
-      int off, n, kv, nt, nm;
-      request_tiles(a, r, off, n, kv, nt, nm);
-      mine = nt * nm * a.g.Hkv;
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int before = carry, all = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) before += warp_sum[w];
-      all += warp_sum[w];
-    }
-    if (r < a.g.R) pre[r] = before + incl - mine;
-    carry += all;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) pre[a.g.R] = carry;
-  __syncthreads();
-}
-
-// The request whose tiles hold tile x (0 <= x < pre[R]).
-__device__ __forceinline__ int request_of(const int* pre, int R, int x) {
-  int lo = 0, hi = R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid + 1] > x) hi = mid;
-    else lo = mid + 1;
-  }
-  return lo;
-}
-
-__device__ __forceinline__ int share_of(int total, int grid) { return (total + grid - 1) / grid; }
-
-// One run of tiles of one unit within a CTA's share.
-struct Segment {
-  int r, off, n, kv, base;
-  int head, row0;    // KV head, first row of the M-tile
-  int t0, t1, nt;    // tiles t0 .. t1 - 1 of nt
-  __device__ __forceinline__ bool whole() const { return t1 - t0 == nt; }
-};
-
-__device__ __forceinline__ Segment segment_at(const TreeArgs& a, const int* pre, int x, int end, int& r) {
-  while (pre[r + 1] <= x) ++r;
-  Segment s;
-  int nm;
-  s.r = r;
-  request_tiles(a, r, s.off, s.n, s.kv, s.nt, nm);
-  s.base = s.kv - s.n;
-  const int y = x - pre[r];
-  const int unit = y / s.nt;
-  s.t0 = y - unit * s.nt;
-  s.t1 = min(s.nt, s.t0 + (end - x));
-  s.head = unit / nm;
-  s.row0 = (unit - s.head * nm) * a.rows;
-  return s;
-}
-
 // ---------------------------------------------------------------------------
 // fragments
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int OFF>
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
@@ -225,38 +114,6 @@ __device__ __forceinline__ void mma16832(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two float32 -> two e4m3 codes (the first in the low byte), nearest even, NaN stays NaN.
-__device__ __forceinline__ uint32_t pack_codes(float a, float b) {
-  unsigned short h;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
-  return h;
-}
-
-// The low or high pair of four e4m3 codes -> two f16 (exact).
-__device__ __forceinline__ uint32_t widen_lo(uint32_t x) {
-  uint32_t u;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(u) : "r"(x));
-  return u;
-}
-__device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
-  uint32_t u;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(u) : "r"(x));
-  return u;
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t u;
-  if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
-  return u;
-}
-
-// What bf16 keeps of (lo, hi) after their bf16 pair `u`.
-__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t u) {
-  return pack2<false>(lo - __uint_as_float(u << 16), hi - __uint_as_float(u & 0xffff0000u));
-}
-
 template <bool E4M3, int D, int NB>
 struct Cfg {
   static constexpr int ES = E4M3 ? 1 : 2;
@@ -277,48 +134,7 @@ struct Cfg {
   static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
-
-// Infinities and NaN that new tokens of this segment hold in four columns of V
-// reach the rows that see them (rare: they entered the products as zeros).
-template <bool E4M3, bool TOKEN, int D>
-__device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg, int t, int d, int tile, float4& acc) {
-  const CacheGeometry& g = a.g;
-  const int32_t* row = g.table + (long long)sg.r * g.max_pages;
-  for (int pos = max(sg.base, sg.t0 * tile); pos < min(sg.kv, sg.t1 * tile); ++pos) {
-    const int j = pos - sg.base;
-    const bool see = a.mask ? (__ldg(a.mask + (long long)(sg.off + t) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u : j <= t;
-    const int page = __ldg(row + (pos >> g.page_shift));
-    if (!see || page < 0 || page >= g.num_pages) continue;
-    const long long slot = ((long long)page << g.page_shift) + (pos & (g.page_size - 1));
-    const long long at = (slot * g.Hkv + sg.head) * D + d;
-    float v[4];
-    if constexpr (E4M3) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(g.v_pool + at);
-      float sc = 1.f;
-      if (TOKEN) sc = __ldg(g.v_scale + (((long long)page * g.Hkv + sg.head) << g.page_shift) + (pos & (g.page_size - 1)));
-      const __half2_raw lo = {(unsigned short)widen_lo(w), (unsigned short)(widen_lo(w) >> 16)};
-      const __half2_raw hi = {(unsigned short)widen_hi(w), (unsigned short)(widen_hi(w) >> 16)};
-      const float2 x = __half22float2(__half2(lo)), y = __half22float2(__half2(hi));
-      v[0] = x.x * sc, v[1] = x.y * sc, v[2] = y.x * sc, v[3] = y.y * sc;
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(g.v_pool + at * 2);
-      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
-      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
-    }
-    if (!isfinite(v[0])) acc.x += v[0];
-    if (!isfinite(v[1])) acc.y += v[1];
-    if (!isfinite(v[2])) acc.z += v[2];
-    if (!isfinite(v[3])) acc.w += v[3];
-  }
-}
 
 // E4M3: cache type; TOKEN: token scales; NB: blocks of 8 rows held by every warp.
 template <bool E4M3, bool TOKEN, int D, int NB>
@@ -582,23 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
 
-    // Which of the 32 positions from base + j0 on (j0 > -32) row gr + 8 b sees, as bits.
-    auto row_sees = [&](int b, int j0) -> uint32_t {
-      const uint32_t cached = j0 < 0 ? (1u << -j0) - 1u : 0u;
-      if (!in[b]) return cached;
-      uint32_t bits;
-      if (a.mask) {
-        const uint32_t* words = a.mask + (long long)(sg.off + tok[b]) * a.mask_words;
-        auto word = [&](int i) -> uint32_t { return i >= 0 && i * 32 < sg.n ? __ldg(words + i) : 0u; };
-        const int i = j0 >> 5;  // (-1 for negative j0)
-        bits = __funnelshift_r(word(i), word(i + 1), j0 & 31);
-      } else {
-        const int seen = tok[b] + 1 - j0;  // (j0 + bit <= tok)
-        bits = seen >= 32 ? 0xffffffffu : seen > 0 ? (1u << seen) - 1u : 0u;
-      }
-      return bits | cached;
-    };
-
     // STEPS blocks of 16 keys of one tile: first position pos0, first key k0 of the
     // tile; SPECIAL: some are new tokens, or slots behind the last one.
     auto update = [&](auto special, int pos0, int k0, uint32_t ka, uint32_t va, const float* ksc, const float* vsc,
@@ -659,10 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < NB; ++b) mx[b] = -INFINITY;
       uint32_t see[SPECIAL ? NB : 1];
       if constexpr (SPECIAL) {
-        const int there = sg.kv - pos0;  // positions behind the last token
-        const uint32_t some = there >= 32 ? 0xffffffffu : there > 0 ? (1u << there) - 1u : 0u;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) see[b] = row_sees(b, pos0 - sg.base) & some;
+        for (int b = 0; b < NB; ++b) see[b] = row_sees(a, sg, in[b], tok[b], pos0);
       }
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
@@ -1041,7 +838,8 @@ int sm_count() {
   return n;
 }
 
-int unit_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 32; }
+// Rows per unit: the kernel here holds 8 or 16, the one for many rows (tree_wide.cu) one or two M-tiles of 128.
+int unit_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 128 ? 128 : 256; }
 
 template <bool E4M3, bool TOKEN, int D, int NB>
 cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
@@ -1051,7 +849,11 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<a.grid, kThreads, smem, s>>>(mk, mv, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t run_merge(const TreeArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.g.total_tokens * a.Hq));
   cfg.blockDim = dim3(kMergeThreads);
@@ -1067,9 +869,7 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
 
 template <bool E4M3, bool TOKEN, int D>
 cudaError_t run_rows(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  if (a.rows == 8) return run<E4M3, TOKEN, D, 1>(a, mk, mv, s);
-  if (a.rows == 16) return run<E4M3, TOKEN, D, 2>(a, mk, mv, s);
-  return run<E4M3, TOKEN, D, 4>(a, mk, mv, s);
+  return a.rows == 8 ? run<E4M3, TOKEN, D, 1>(a, mk, mv, s) : run<E4M3, TOKEN, D, 2>(a, mk, mv, s);
 }
 
 size_t pad256(size_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -1099,7 +899,7 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   const double scale = t.softmax_scale > 0.f ? (double)t.softmax_scale : 1.0 / std::sqrt((double)g.d);
   a.scale_log2 = (float)(scale * 1.4426950408889634);
   a.grid = sm_count();
-  a.tile = kTileBytes / (g.d * (g.e4m3 ? 1 : 2));
+  a.tile = a.rows <= 16 ? kTileBytes / (g.d * (g.e4m3 ? 1 : 2)) : 128;
   const size_t rows = (size_t)2 * a.grid * a.rows;
   a.part_o = static_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pad256(rows * g.d * sizeof(float)));
@@ -1115,8 +915,10 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
       !encode_tiled(&mv, type, 4, g.v_pool, dims, strides, box, promotion))
     return FP_ERR_CUDA;
   cudaError_t e;
-  if (g.e4m3) e = g.token_scale ? run_rows<true, true, 128>(a, mk, mv, s) : run_rows<true, false, 128>(a, mk, mv, s);
+  if (a.rows > 16) e = launch_wide(a, mk, mv, s);
+  else if (g.e4m3) e = g.token_scale ? run_rows<true, true, 128>(a, mk, mv, s) : run_rows<true, false, 128>(a, mk, mv, s);
   else e = g.d == 128 ? run_rows<false, false, 128>(a, mk, mv, s) : run_rows<false, false, 64>(a, mk, mv, s);
+  if (e == cudaSuccess) e = g.d == 128 ? run_merge<128>(a, s) : run_merge<64>(a, s);
   if (e != cudaSuccess) {
     set_last_error("tree attention launch", (int)e, cudaGetErrorString(e));
     return FP_ERR_CUDA;

@@ -1,0 +1,233 @@
+// What the kernels of the tree attention share: their arguments, the axis of key
+// tiles that is cut over the SMs, and small conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.cuh"
+#include "sm100.cuh"
+
+namespace fp {
+namespace tree {
+
+// The reference of a row's exponents rises only when its maximum exceeds it by
+// more than kSlack (log2 units): nearly every step of a short run would raise
+// the exact maximum of one of the rows, and each rise rescales O. f16 weights
+// (e4m3 caches) carry a factor 2^kShift: at most 2^15, and normal down to 2^-22
+// below the reference.
+constexpr float kSlack = 7.f, kShift = 8.f;
+
+struct TreeArgs {
+  CacheGeometry g;
+  int Hq, G;
+  int max_tokens;
+  int rows;               // rows per M-tile unit
+  int tile;               // keys per tile
+  const uint32_t* mask;
+  int mask_words;
+  const __nv_bfloat16* q;
+  long long q_stride;
+  __nv_bfloat16* o;
+  float* lse;
+  float scale_log2;
+  float* part_o;          // [2 * grid][rows][d]
+  float* part_lse;        // [2 * grid][rows], base 2
+  int grid;
+};
+
+// ---------------------------------------------------------------------------
+// the axis of tiles
+// ---------------------------------------------------------------------------
+// Tiles of the keys of request r, and M-tile units per KV head (0 for a request
+// that is empty, or rejected).
+__device__ __forceinline__ void request_tiles(const TreeArgs& a, int r, int& off, int& n, int& kv, int& nt, int& nm) {
+  nt = nm = 0;
+  if (!cache_span(a.g, r, off, n, kv)) return;
+  if (n > a.max_tokens) {
+    atomicOr(a.g.status, FP_DEV_BAD_SEQLENS);
+    n = 0;
+  }
+  if (n == 0) return;
+  nt = (kv + a.tile - 1) / a.tile;
+  nm = (n * a.G + a.rows - 1) / a.rows;
+}
+
+// Exclusive prefix of the requests' tile counts into pre[0 .. R] (all threads of
+// the block; `warp_sum` has one int per warp). The host bounds the total by INT_MAX.
+__device__ __forceinline__ void prefix_tiles(const TreeArgs& a, int* pre, int* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int carry = 0;
+  for (int r0 = 0; r0 < a.g.R; r0 += blockDim.x) {
+    const int r = r0 + threadIdx.x;
+    int mine = 0;
+    if (r < a.g.R) {
+      int off, n, kv, nt, nm;
+      request_tiles(a, r, off, n, kv, nt, nm);
+      mine = nt * nm * a.g.Hkv;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = carry, all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (r < a.g.R) pre[r] = before + incl - mine;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) pre[a.g.R] = carry;
+  __syncthreads();
+}
+
+// The request whose tiles hold tile x (0 <= x < pre[R]).
+__device__ __forceinline__ int request_of(const int* pre, int R, int x) {
+  int lo = 0, hi = R - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid + 1] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int share_of(int total, int grid) { return (total + grid - 1) / grid; }
+
+// One run of tiles of one unit within a CTA's share.
+struct Segment {
+  int r, off, n, kv, base;
+  int head, row0;    // KV head, first row of the M-tile
+  int t0, t1, nt;    // tiles t0 .. t1 - 1 of nt
+  __device__ __forceinline__ bool whole() const { return t1 - t0 == nt; }
+};
+
+__device__ __forceinline__ Segment segment_at(const TreeArgs& a, const int* pre, int x, int end, int& r) {
+  while (pre[r + 1] <= x) ++r;
+  Segment s;
+  int nm;
+  s.r = r;
+  request_tiles(a, r, s.off, s.n, s.kv, s.nt, nm);
+  s.base = s.kv - s.n;
+  const int y = x - pre[r];
+  const int unit = y / s.nt;
+  s.t0 = y - unit * s.nt;
+  s.t1 = min(s.nt, s.t0 + (end - x));
+  s.head = unit / nm;
+  s.row0 = (unit - s.head * nm) * a.rows;
+  return s;
+}
+
+// Which of the 32 positions from pos0 on a row of token `tok` sees, as bits (`in`: the row exists).
+__device__ __forceinline__ uint32_t row_sees(const TreeArgs& a, const Segment& sg, bool in, int tok, int pos0) {
+  const int there = sg.kv - pos0;  // positions behind the last token
+  const uint32_t some = there >= 32 ? 0xffffffffu : there > 0 ? (1u << there) - 1u : 0u;
+  const int j0 = pos0 - sg.base;   // the first position as a new token
+  if (j0 <= -32) return some;
+  const uint32_t cached = j0 < 0 ? (1u << -j0) - 1u : 0u;
+  uint32_t bits = 0;
+  if (in && a.mask) {
+    const uint32_t* words = a.mask + (long long)(sg.off + tok) * a.mask_words;
+    auto word = [&](int i) -> uint32_t { return i >= 0 && i * 32 < sg.n ? __ldg(words + i) : 0u; };
+    const int i = j0 >> 5;  // (-1 for negative j0)
+    bits = __funnelshift_r(word(i), word(i + 1), j0 & 31);
+  } else if (in) {
+    const int seen = tok + 1 - j0;  // (j0 + bit <= tok)
+    bits = seen >= 32 ? 0xffffffffu : seen > 0 ? (1u << seen) - 1u : 0u;
+  }
+  return (bits | cached) & some;
+}
+
+// ---------------------------------------------------------------------------
+// conversions and copies
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two float32 -> two e4m3 codes (the first in the low byte), nearest even, NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_codes(float a, float b) {
+  unsigned short h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+  return h;
+}
+
+// The low or high pair of four e4m3 codes -> two f16 (exact).
+__device__ __forceinline__ uint32_t widen_lo(uint32_t x) {
+  uint32_t u;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(u) : "r"(x));
+  return u;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
+  uint32_t u;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(u) : "r"(x));
+  return u;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t u;
+  if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+  return u;
+}
+
+// What bf16 keeps of (lo, hi) after their bf16 pair `u`.
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t u) {
+  return pack2<false>(lo - __uint_as_float(u << 16), hi - __uint_as_float(u & 0xffff0000u));
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Infinities and NaN that new tokens of this segment hold in four columns of V
+// reach the rows that see them (rare: they entered the products as zeros).
+template <bool E4M3, bool TOKEN, int D>
+__device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg, int t, int d, int tile, float4& acc) {
+  const CacheGeometry& g = a.g;
+  const int32_t* row = g.table + (long long)sg.r * g.max_pages;
+  for (int pos = max(sg.base, sg.t0 * tile); pos < min(sg.kv, sg.t1 * tile); ++pos) {
+    const int j = pos - sg.base;
+    const bool see = a.mask ? (__ldg(a.mask + (long long)(sg.off + t) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u : j <= t;
+    const int page = __ldg(row + (pos >> g.page_shift));
+    if (!see || page < 0 || page >= g.num_pages) continue;
+    const long long slot = ((long long)page << g.page_shift) + (pos & (g.page_size - 1));
+    const long long at = (slot * g.Hkv + sg.head) * D + d;
+    float v[4];
+    if constexpr (E4M3) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(g.v_pool + at);
+      float sc = 1.f;
+      if (TOKEN) sc = __ldg(g.v_scale + (((long long)page * g.Hkv + sg.head) << g.page_shift) + (pos & (g.page_size - 1)));
+      const __half2_raw lo = {(unsigned short)widen_lo(w), (unsigned short)(widen_lo(w) >> 16)};
+      const __half2_raw hi = {(unsigned short)widen_hi(w), (unsigned short)(widen_hi(w) >> 16)};
+      const float2 x = __half22float2(__half2(lo)), y = __half22float2(__half2(hi));
+      v[0] = x.x * sc, v[1] = x.y * sc, v[2] = y.x * sc, v[3] = y.y * sc;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(g.v_pool + at * 2);
+      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+    }
+    if (!isfinite(v[0])) acc.x += v[0];
+    if (!isfinite(v[1])) acc.y += v[1];
+    if (!isfinite(v[2])) acc.z += v[2];
+    if (!isfinite(v[3])) acc.w += v[3];
+  }
+}
+
+// The kernel for many rows (tree_wide.cu): a.rows is 128 or 256.
+cudaError_t launch_wide(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s);
+
+}  // namespace tree
+}  // namespace fp

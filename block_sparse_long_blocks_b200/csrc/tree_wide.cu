@@ -1,0 +1,829 @@
+// Attention over the paged cache for many rows: more than 16 (token, head) rows
+// per request and KV head, as larger trees and chunks of a prompt bring.
+//
+// The mathematics, the axis of key tiles, the shares, partial rows and their
+// combination are those of tree.cu. Here an M-tile has 128 rows, one per thread
+// of a softmax warpgroup, and both products run on tcgen05:
+//   S = Q K^T (tensor memory), P = 2^(x - ref) written over S, O += P V.
+// PAIR (more than 128 rows): a unit has two M-tiles; every K and V tile serves
+// both, and one's softmax overlaps the other's products. Otherwise the unit has
+// one M-tile, and the two warpgroups take its key tiles in turn, each with its
+// own O, which meet at the segment's end: HBM, not the softmax of one
+// warpgroup, then bounds it.
+//
+// Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warp 8 TMA
+// producer, warp 9 MMA issuer, warps 10-11 converters. Operands are 16-bit:
+// bf16 caches multiply bf16 (P as hi + lo: two products, 16 bits of weight);
+// e4m3 caches are widened exactly to f16 by the converters, q goes to f16 as
+// q * 2^e with e per row such that max |q| lies in [2^14, 2^15), P to f16.
+// The converters also make the tiles that hold new tokens or end behind the
+// last one safe to multiply: V rows behind the last token become zeros, and so
+// do infinities and NaN of new tokens, which only some rows see (those are
+// added to the rows that see them at the end).
+// Every wait is bounded; after one ran out every role leaves its loop, the MMA
+// issuer and the producer wait for what they have in flight, outputs are
+// invalid and FP_DEV_TIMEOUT is set.
+#include <cuda.h>
+
+#include <climits>
+
+#include "tree.cuh"
+
+namespace fp {
+namespace tree {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kConvertWarp = 10;
+// 2 x 128 x 200 + 128 x 104 = 384 x 168
+constexpr uint32_t kSoftmaxRegs = 200, kControlRegs = 104;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * 168, "register split exceeds the launch");
+constexpr int kKeys = 128;           // per tile
+constexpr int kChunk = kKeys * 128;  // bytes of a tile's 128-byte-wide chunk
+constexpr int kCleaned = 8;          // > V tiles that the ring can hold
+constexpr int kFlags = 8;            // > segments that the ring can reach into
+constexpr int kScales = 4;           // tiles whose token scales are kept (see the converters)
+
+template <bool E4M3, int D, bool PAIR>
+struct Cfg {
+  static constexpr int ES = E4M3 ? 1 : 2;
+  static constexpr int CH = D / 64;                     // chunks of a 16-bit tile
+  static constexpr int TILE = CH * kChunk;              // bytes of a 16-bit K, V or Q tile
+  static constexpr int LOAD_CH = D * ES / 128;          // chunks of a loaded tile
+  static constexpr int CH_ELEMS = 128 / ES;
+  static constexpr int Q = (PAIR ? 2 : 1) * TILE;
+  static constexpr int SLOTS = E4M3 ? 3 : D == 64 ? 8 : PAIR ? 4 : 5;   // 16-bit tiles
+  static constexpr int RAW_SLOTS = E4M3 ? (PAIR ? 2 : 4) : 0;           // e4m3 tiles as loaded, + their scales
+  static constexpr int RAW_SLOT = kChunk + 1024;
+  static constexpr int AHEAD = PAIR ? 1 : 2;            // K tiles loaded before the first V tile
+  static constexpr int LOAD_SLOTS = E4M3 ? RAW_SLOTS : SLOTS;
+  static constexpr int LOAD_SLOT = E4M3 ? RAW_SLOT : TILE;
+  static constexpr int NUM_BARS = 2 * (SLOTS + RAW_SLOTS) + 2 + 2 + 4 + 2 + kCleaned + 3;
+  static constexpr int SMEM_FIXED = 1024 + Q + SLOTS * TILE + RAW_SLOTS * RAW_SLOT +
+                                    (E4M3 ? kScales * 2 * kKeys * 4 : 0) + 128 * 16 + NUM_BARS * 8 + 160;
+  static constexpr int COLS = Q / 512 < D ? Q / 512 : D;  // columns of O per round in which two warpgroups' O meet
+  static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
+  static_assert(COLS % 32 == 0 && D % COLS == 0, "rounds of whole TMEM loads");
+};
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Where a segment's tiles lie in the sequence of ring items (K and V tiles).
+// PAIR: K0 V0 K1 V1 ...; otherwise one more K tile goes ahead: K0 K1 V0 K2 V1 ...
+template <bool PAIR>
+__device__ __forceinline__ int item_k(int i) { return PAIR ? 2 * i : max(0, 2 * i - 1); }
+template <bool PAIR>
+__device__ __forceinline__ int item_v(int i, int nt) { return PAIR ? 2 * i + 1 : min(2 * i + 2, 2 * nt - 1); }
+
+template <bool E4M3, bool TOKEN, int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+  using C = Cfg<E4M3, D, PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sT = sQ + C::Q;                        // 16-bit tiles
+  uint8_t* sR = sT + C::SLOTS * C::TILE;          // e4m3 tiles as loaded
+  float* s_ksc = reinterpret_cast<float*>(sR + C::RAW_SLOTS * C::RAW_SLOT);  // [kScales][kKeys]
+  float* s_vsc = s_ksc + (E4M3 ? kScales * kKeys : 0);
+  float4* s_half = reinterpret_cast<float4*>(s_vsc + (E4M3 ? kScales * kKeys : 0));  // [128] second warpgroup's ref, l, factor
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_half + 128);
+  uint64_t* empty = full + C::SLOTS;
+  uint64_t* rfull = empty + C::SLOTS;
+  uint64_t* rempty = rfull + C::RAW_SLOTS;
+  uint64_t* q_full = rempty + C::RAW_SLOTS;       // [2]
+  uint64_t* s_full = q_full + 2;                  // [2]
+  uint64_t* p_full = s_full + 2;                  // [warpgroup][half of the keys]
+  uint64_t* o_full = p_full + 4;                  // [2]
+  uint64_t* cleaned = o_full + 2;                 // [kCleaned]: V tiles with new tokens or a ragged end, in turn
+  uint64_t* half_full = cleaned + kCleaned;
+  uint64_t* half_empty = half_full + 1;
+  uint64_t* drain = half_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* warp_sum = reinterpret_cast<int*>(tmem_slot + 2);             // [12]
+  volatile uint32_t* s_vmax = tmem_slot + 14;                        // [kScales][2]
+  volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 22);  // [kFlags][2]
+  int* pre = reinterpret_cast<int*>(tmem_slot + 40);                 // [R + 1]
+
+  const CacheGeometry& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(full + s, E4M3 ? 64 : 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < C::RAW_SLOTS; ++s) {
+      mbar_init(rfull + s, 1);
+      mbar_init(rempty + s, 64);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(q_full + w, PAIR ? 128 : 256);
+      mbar_init(s_full + w, 1);
+      mbar_init(p_full + 2 * w, 128);
+      mbar_init(p_full + 2 * w + 1, 128);
+      mbar_init(o_full + w, 1);
+    }
+    for (int k = 0; k < kCleaned; ++k) mbar_init(cleaned + k, 64);
+    mbar_init(half_full, 128);
+    mbar_init(half_empty, 128);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  prefix_tiles(a, pre, warp_sum);  // (its barriers publish the initialisation above)
+  const int total = pre[g.R];
+  const int share = share_of(total, a.grid);
+  const long long x_first = (long long)blockIdx.x * share;
+  if (x_first >= total) return;
+  const int x_begin = (int)x_first, x_end = min(total, x_begin + share);
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp >= 8) reg_dealloc<kControlRegs>();
+
+  bool ok = true;
+  int r = request_of(pre, g.R, x_begin);
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    uint64_t* lfull = E4M3 ? rfull : full;
+    uint64_t* lempty = E4M3 ? rempty : empty;
+    uint8_t* ring = E4M3 ? sR : sT;
+    const int sub_rows = min(g.page_size, kKeys), sub_max = kKeys / sub_rows;  // sub_max <= 8
+    int slot = 0, issued = 0;
+    uint32_t phase = 0;
+    for (int x = x_begin; x < x_end && ok;) {
+      const Segment sg = segment_at(a, pre, x, x_end, r);
+      const int nt = sg.t1 - sg.t0;
+      x += nt;
+      const int32_t* row = g.table + (long long)sg.r * g.max_pages;
+      auto page_at = [&](int i) {  // the page of this lane's part of tile i of the segment
+        const int tok = (sg.t0 + i) * kKeys + lane * sub_rows;
+        return (i < nt && lane < sub_max && tok < sg.kv) ? __ldg(row + (tok >> g.page_shift)) : -1;
+      };
+      auto load = [&](bool v, int i, int page) {
+        const int tok = (sg.t0 + i) * kKeys + lane * sub_rows;
+        const bool mine = lane < sub_max && tok < sg.kv;
+        const int subs = min(sub_max, (sg.kv - (sg.t0 + i) * kKeys + sub_rows - 1) / sub_rows);
+        const bool bad = mine && (page < 0 || page >= g.num_pages);
+        if (bad) {
+          atomicOr(g.status, FP_DEV_BAD_PAGE);
+          page = g.num_pages;  // outside the pool: the copy fills zeros
+        }
+        ok = mbar_wait<true>(lempty + slot, phase ^ 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+        if (!ok) return;
+        uint8_t* dst = ring + slot * C::LOAD_SLOT;
+        if (lane == 0) {
+          uint32_t bytes = (uint32_t)(subs * sub_rows) * (D * C::ES);
+          if (TOKEN) bytes += (uint32_t)(subs * sub_rows) * 4u;
+          mbar_arrive_expect_tx(lfull + slot, bytes);
+        }
+        __syncwarp();
+        if (mine) {
+          const int at = tok & (g.page_size - 1);
+#pragma unroll
+          for (int ch = 0; ch < C::LOAD_CH; ++ch)
+            tma_load_4d(dst + ch * kChunk + lane * sub_rows * 128, v ? &tmV : &tmK, lfull + slot, ch * C::CH_ELEMS,
+                        sg.head, at, page);
+          if (TOKEN) {
+            const float* sc = v ? g.v_scale : g.k_scale;
+            const long long pg = bad ? 0 : page;  // (a bad page's codes are zeros: any scale does)
+            bulk_load(dst + kChunk + lane * sub_rows * 4, sc + ((pg * g.Hkv + sg.head) << g.page_shift) + at,
+                      (uint32_t)sub_rows * 4u, lfull + slot);
+          }
+        }
+        ++issued;
+        if (++slot == C::LOAD_SLOTS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      };
+      int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2);
+      load(false, 0, p0);
+      if (!PAIR && ok && nt > 1) load(false, 1, p1);
+      for (int i = 0; i < nt && ok; ++i) {
+        const int p3 = page_at(i + 3);
+        load(true, i, p0);
+        if (ok && i + C::AHEAD < nt) load(false, i + C::AHEAD, PAIR ? p1 : p2);
+        p0 = p1;
+        p1 = p2;
+        p2 = p3;
+      }
+    }
+    // every copy lands before the CTA's shared memory is released
+    if (lane == 0) {
+      for (int k = 0; k < min(issued, C::LOAD_SLOTS); ++k) {
+        const int i = issued - 1 - k;
+        mbar_drain(lfull + i % C::LOAD_SLOTS, (uint32_t)((i / C::LOAD_SLOTS) & 1), g.status, FP_DEV_TIMEOUT);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t fmt = E4M3 ? 0u : 1u;  // f16 or bf16
+      const uint32_t idesc_qk = instr_desc(fmt, 128, kKeys, 0, 0);
+      const uint32_t idesc_pv = instr_desc(fmt, 128, D, 0, 1);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sT), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(sT), kChunk, 1024);
+      auto issue_qk = [&](int w, int slot) {
+        const uint64_t a0 = dQ + (uint64_t)(((PAIR ? w : 0) * C::TILE) >> 4);
+        const uint64_t b0 = dK + (uint64_t)((slot * C::TILE) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (uint32_t)((ks >> 2) * kChunk + (ks & 3) * 32) >> 4;
+          umma_f16_ss(tmem + w * 128, a0 + off, b0 + off, idesc_qk, ks > 0);
+        }
+      };
+      // P of a half of the keys: f16, 32 columns; or bf16 hi, 32 columns, then lo, 32 columns
+      auto issue_pv = [&](int w, int slot, bool acc, int hf) {
+        const uint64_t b0 = dV + (uint64_t)((slot * C::TILE) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 32; ++ks) {
+          const uint64_t bd = b0 + ((uint32_t)((hf * (kKeys / 32) + ks) * 16 * 128) >> 4);
+          const uint32_t pt = tmem + w * 128 + hf * (E4M3 ? 32 : 64) + ks * 8;
+          umma_f16_ts(tmem + 256 + w * 128, pt, bd, idesc_pv, (acc || ks > 0) ? 1u : 0u);
+          if (!E4M3) umma_f16_ts(tmem + 256 + w * 128, pt + 32, bd, idesc_pv, 1u);
+        }
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = mbar_wait(bar, parity, abort_flag, g.status, FP_DEV_TIMEOUT);
+        return ok;
+      };
+      int base = 0, qn = 0, cn = 0, pn[2] = {0, 0};
+      for (int x = x_begin; x < x_end && ok;) {
+        const Segment sg = segment_at(a, pre, x, x_end, r);
+        const int nt = sg.t1 - sg.t0;
+        x += nt;
+        auto wait_item = [&](int item) { return wait(full + item % C::SLOTS, (uint32_t)(item / C::SLOTS) & 1u); };
+        if (!wait(q_full, (uint32_t)qn & 1u)) break;
+        if (PAIR && !wait(q_full + 1, (uint32_t)qn & 1u)) break;
+        ++qn;
+        if (!wait_item(base)) break;
+        tc_fence_after();
+        issue_qk(0, base % C::SLOTS);
+        umma_commit(s_full + 0);
+        if (PAIR) {
+          issue_qk(1, base % C::SLOTS);
+          umma_commit(s_full + 1);
+        }
+        umma_commit(empty + base % C::SLOTS);
+        if (!PAIR && nt > 1) {
+          const int item = base + 1;
+          if (!wait_item(item)) break;
+          tc_fence_after();
+          issue_qk(1, item % C::SLOTS);
+          umma_commit(s_full + 1);
+          umma_commit(empty + item % C::SLOTS);
+        }
+        for (int i = 0; i < nt; ++i) {
+          const int vi = base + item_v<PAIR>(i, nt), vslot = vi % C::SLOTS;
+          if (!E4M3 && (sg.t0 + i + 1) * kKeys > sg.base) {  // cleaned after its copy landed
+            if (!wait(cleaned + cn % kCleaned, (uint32_t)(cn / kCleaned) & 1u)) break;
+            ++cn;
+          } else if (!wait_item(vi)) {
+            break;
+          }
+          const bool more = i + C::AHEAD < nt;
+          const int ki = base + item_k<PAIR>(i + C::AHEAD), kslot = ki % C::SLOTS;
+          bool k_there = !more;
+          const int w0 = PAIR ? 0 : i & 1, w1 = PAIR ? 1 : w0;
+#pragma unroll 1
+          for (int w = w0; w <= w1 && ok; ++w) {
+            const bool acc = PAIR ? i > 0 : i > 1;
+            if (!wait(p_full + 2 * w, (uint32_t)pn[w] & 1u)) break;
+            tc_fence_after();
+            issue_pv(w, vslot, acc, 0);
+            // the next K tile is waited for while the second half is computed
+            if (!k_there) {
+              if (!wait_item(ki)) break;
+              k_there = true;
+            }
+            if (!wait(p_full + 2 * w + 1, (uint32_t)pn[w] & 1u)) break;
+            ++pn[w];
+            tc_fence_after();
+            issue_pv(w, vslot, true, 1);
+            if (w == w1) umma_commit(empty + vslot);
+            if (more) {
+              issue_qk(w, kslot);
+              umma_commit(s_full + w);
+              if (w == w1) umma_commit(empty + kslot);
+            } else if (PAIR) {
+              umma_commit(o_full + w);
+            }
+          }
+          if (!ok) break;
+        }
+        if (!ok) break;
+        if (!PAIR) {
+          umma_commit(o_full + 0);
+          umma_commit(o_full + 1);
+        }
+        base += 2 * nt;
+      }
+      // every MMA this thread issued has completed once `drain` flips
+      umma_commit(drain);
+      mbar_drain(drain, 0u, g.status, FP_DEV_TIMEOUT);
+    }
+  } else if (warp >= kConvertWarp) {
+    // ------------------------------------------------------------------ converters
+    const int ct = threadIdx.x - kConvertWarp * 32, cw = warp - kConvertWarp;
+    int base = 0, rn = 0, tn = 0, cn = 0, segment = 0;
+    for (int x = x_begin; x < x_end && ok; ++segment) {
+      const Segment sg = segment_at(a, pre, x, x_end, r);
+      const int nt = sg.t1 - sg.t0;
+      x += nt;
+      bool fresh = true;  // the segment's flag is not cleared yet
+      auto flag_odd = [&](bool odd) {
+        volatile int* f = s_odd + segment % kFlags * 2 + cw;
+        if (fresh && lane == 0) *f = 0;
+        fresh = false;
+        __syncwarp();
+        if (odd) *f = 1;
+      };
+      if constexpr (!E4M3) {
+        for (int i = max(0, sg.base / kKeys - sg.t0); i < nt; ++i) {
+          const int vi = base + item_v<PAIR>(i, nt);
+          ok = mbar_wait<true>(full + vi % C::SLOTS, (uint32_t)(vi / C::SLOTS) & 1u, abort_flag, g.status,
+                               FP_DEV_TIMEOUT);
+          if (!ok) break;
+          uint8_t* tile = sT + (vi % C::SLOTS) * C::TILE;
+          bool odd = false;
+          for (int q = ct; q < C::CH * kKeys * 8; q += 64) {  // (where a granule lies in its row does not matter)
+            const int pos = (sg.t0 + i) * kKeys + ((q >> 3) & (kKeys - 1));
+            if (pos < sg.base) continue;
+            uint4* p = reinterpret_cast<uint4*>(tile) + q;
+            if (pos >= sg.kv) {
+              *p = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            const uint4 v = *p;
+            const uint32_t m = 0x7f807f80u;
+            const uint32_t b0 = __vcmpeq2(v.x & m, m), b1 = __vcmpeq2(v.y & m, m), b2 = __vcmpeq2(v.z & m, m),
+                           b3 = __vcmpeq2(v.w & m, m);
+            if (b0 | b1 | b2 | b3) {
+              odd = true;
+              *p = make_uint4(v.x & ~b0, v.y & ~b1, v.z & ~b2, v.w & ~b3);
+            }
+          }
+          flag_odd(odd);
+          fence_async();
+          mbar_arrive(cleaned + cn % kCleaned);
+          ++cn;
+        }
+      } else {
+        for (int item = 0; item < 2 * nt && ok; ++item, ++rn) {
+          // the item's kind and tile: item_k and item_v the other way round
+          bool v;
+          int i;
+          if (PAIR) {
+            v = item & 1;
+            i = item >> 1;
+          } else if (item < 2 || item == 2 * nt - 1) {
+            v = item == 2 * nt - 1;
+            i = v ? nt - 1 : item;
+          } else {
+            v = !(item & 1);
+            i = v ? item / 2 - 1 : (item + 1) / 2;
+          }
+          const int rs = rn % C::RAW_SLOTS, ts = (base + item) % C::SLOTS;
+          ok = mbar_wait<true>(rfull + rs, (uint32_t)(rn / C::RAW_SLOTS) & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+          if (!ok) break;
+          ok = mbar_wait<true>(empty + ts, ((uint32_t)((base + item) / C::SLOTS) & 1u) ^ 1u, abort_flag, g.status,
+                               FP_DEV_TIMEOUT);
+          if (!ok) break;
+          const uint8_t* src = sR + rs * C::RAW_SLOT;
+          uint8_t* dst = sT + ts * C::TILE;
+          const int pos0 = (sg.t0 + i) * kKeys;
+          const bool special = v && pos0 + kKeys > sg.base;
+          bool odd = false;
+#pragma unroll 4
+          for (int q = ct; q < kKeys * 8; q += 64) {
+            const int key = q >> 3, g8 = q & 7, sw = key & 7;
+            uint4 w = *reinterpret_cast<const uint4*>(src + key * 128 + ((g8 ^ sw) << 4));
+            if (special && pos0 + key >= sg.base) {
+              const uint32_t m = 0x7f7f7f7fu;
+              if (pos0 + key >= sg.kv) w = make_uint4(0, 0, 0, 0);
+              const uint32_t b0 = __vcmpeq4(w.x & m, m), b1 = __vcmpeq4(w.y & m, m), b2 = __vcmpeq4(w.z & m, m),
+                             b3 = __vcmpeq4(w.w & m, m);
+              odd |= (b0 | b1 | b2 | b3) != 0;
+              w = make_uint4(w.x & ~b0, w.y & ~b1, w.z & ~b2, w.w & ~b3);
+            }
+            uint8_t* row = dst + (g8 >> 2) * kChunk + key * 128;
+            const int p = 2 * (g8 & 3);
+            *reinterpret_cast<uint4*>(row + ((p ^ sw) << 4)) =
+                make_uint4(widen_lo(w.x), widen_hi(w.x), widen_lo(w.y), widen_hi(w.y));
+            *reinterpret_cast<uint4*>(row + (((p + 1) ^ sw) << 4)) =
+                make_uint4(widen_lo(w.z), widen_hi(w.z), widen_lo(w.w), widen_hi(w.w));
+          }
+          if constexpr (TOKEN) {
+            // Scales of the last kScales tiles: tile tn + i's are written when the slot of the
+            // item three before its own is free, so the softmax of the tile four before it is over.
+            const int at = (tn + i) % kScales;
+            float2 sc = *reinterpret_cast<const float2*>(src + kChunk + ct * 8);
+            if (special) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& y = e ? sc.y : sc.x;
+                const int pos = pos0 + 2 * ct + e;
+                if (pos >= sg.kv) {
+                  y = 0.f;
+                } else if (pos >= sg.base && !(y < INFINITY)) {
+                  y = 0.f;
+                  odd = true;
+                }
+              }
+            }
+            *reinterpret_cast<float2*>((v ? s_vsc : s_ksc) + at * kKeys + 2 * ct) = sc;
+            if (v) {
+              // (scales are not negative: they compare as integers)
+              const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(sc.x), __float_as_uint(sc.y)));
+              if (lane == 0) s_vmax[at * 2 + cw] = top;
+            }
+          }
+          if (special) flag_odd(odd);
+          fence_async();
+          mbar_arrive(full + ts);
+          mbar_arrive(rempty + rs);
+        }
+      }
+      base += 2 * nt;
+      tn += nt;
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax warpgroups
+    reg_alloc<kSoftmaxRegs>();
+    const int w = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)(row & ~31) << 16;
+    const uint32_t tS = tmem + lane_base + w * 128;
+    const uint32_t tO = tmem + lane_base + 256 + w * 128;
+    int base = 0, tn = 0, sn = 0, on = 0, hn = 0, segment = 0;
+    for (int x = x_begin; x < x_end; ++segment) {
+      const Segment sg = segment_at(a, pre, x, x_end, r);
+      const int nt = sg.t1 - sg.t0;
+      x += nt;
+      const int lr = PAIR ? w * 128 + row : row, rho = sg.row0 + lr;
+      const bool in = rho < sg.n * a.G;
+      const int tok = in ? rho / a.G : 0, h = in ? rho - tok * a.G : 0;
+      // ---- this thread's row of Q (of a shared tile: this warpgroup's chunk)
+      float sl2 = a.scale_log2;
+      {
+        const uint4* qp = reinterpret_cast<const uint4*>(a.q + (long long)(sg.off + tok) * a.q_stride +
+                                                         (sg.head * a.G + h) * D);
+        uint8_t* dst = sQ + (PAIR ? w * C::TILE : 0) + row * 128;
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int ch = 0; ch < C::CH; ++ch) {
+            if (!PAIR && ch != w) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(dst + ch * kChunk + (((i ^ row) & 7) << 4)) =
+                  in ? __ldg(qp + ch * 8 + i) : make_uint4(0, 0, 0, 0);
+          }
+        } else {
+          uint4 v[16];
+          float mx = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[i] = in ? __ldg(qp + i) : make_uint4(0, 0, 0, 0);
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+          }
+          // times 2^(14 - floor(log2 max)); rows of zeros, infinities or below 2^-100 take the limits
+          int e2 = (int)((__float_as_uint(mx) >> 23) & 255u) - 127;
+          e2 = mx == 0.f || e2 > 127 ? 14 : max(e2, -100);
+          const float up = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
+          sl2 *= __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+          if (!TOKEN) sl2 *= __ldg(g.k_scale + sg.head);
+          if (sl2 == 0.f) sl2 = 1.2e-38f;  // (0 * -inf of a masked key would be NaN)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (!PAIR && (i >> 3) != w) continue;
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              f[e] = pack2<true>(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+            *reinterpret_cast<uint4*>(dst + (i >> 3) * kChunk + (((i ^ row) & 7) << 4)) =
+                make_uint4(f[0], f[1], f[2], f[3]);
+          }
+        }
+        fence_async();
+        mbar_arrive(q_full + (PAIR ? w : 0));
+      }
+      float v_mul = 1.f;  // what O is multiplied by at the end
+      if (E4M3 && !TOKEN) v_mul = __ldg(g.v_scale + sg.head);
+
+      float ref = -INFINITY, l = 0.f;
+      uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
+      for (int i = PAIR ? 0 : w; i < nt; i += PAIR ? 1 : 2) {
+        ok = mbar_wait<true>(s_full + w, (uint32_t)sn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+        if (!ok) break;
+        ++sn;
+        tc_fence_after();
+        const int pos0 = (sg.t0 + i) * kKeys;
+        float s[kKeys];
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+        {
+          uint32_t sr[kKeys];
+          tmem_ld32(tS, sr);
+          tmem_ld32(tS + 32, sr + 32);
+          tmem_wait_ld();
+          tmem_ld32(tS + 64, sr + 64);
+          tmem_ld32(tS + 96, sr + 96);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            if (hf == 1) tmem_wait_ld();
+#pragma unroll
+            for (int c = hf * 64; c < (hf + 1) * 64; ++c) s[c] = __uint_as_float(sr[c]);
+            if constexpr (TOKEN) {
+              const float* sc = s_ksc + (tn + i) % kScales * kKeys;
+#pragma unroll
+              for (int c = hf * 64; c < (hf + 1) * 64; c += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(sc + c);
+                f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), f2_pack(f.x, f.y)), s[c], s[c + 1]);
+                f2_unpack(f2_mul(f2_pack(s[c + 2], s[c + 3]), f2_pack(f.z, f.w)), s[c + 2], s[c + 3]);
+              }
+            }
+            if (pos0 + kKeys > sg.base) {  // new tokens, or slots behind the last one
+#pragma unroll
+              for (int c0 = hf * 64; c0 < (hf + 1) * 64; c0 += 32) {
+                const uint32_t see = row_sees(a, sg, in, tok, pos0 + c0);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(see >> c & 1u)) s[c0 + c] = -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int c = hf * 64; c < (hf + 1) * 64; c += 8) {
+              m0 = fmaxf(fmaxf(m0, s[c]), s[c + 1]);
+              m1 = fmaxf(fmaxf(m1, s[c + 2]), s[c + 3]);
+              m2 = fmaxf(fmaxf(m2, s[c + 4]), s[c + 5]);
+              m3 = fmaxf(fmaxf(m3, s[c + 6]), s[c + 7]);
+            }
+          }
+        }
+        const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+        float f = 1.f;
+        if (mx > ref + kSlack) {
+          f = exp2_fast(ref - mx);
+          ref = mx;
+          l *= f;
+        }
+        float inv_ref = 1.f;
+        if constexpr (TOKEN) {
+          const int vi = base + item_v<PAIR>(i, nt);  // V's scales are there once it is converted
+          ok = mbar_wait<true>(full + vi % C::SLOTS, (uint32_t)(vi / C::SLOTS) & 1u, abort_flag, g.status,
+                               FP_DEV_TIMEOUT);
+          if (!ok) break;
+          const int at = (tn + i) % kScales;
+          const uint32_t top = max(s_vmax[at * 2], s_vmax[at * 2 + 1]);
+          // the next power of two above it, within 2^-100 .. 2^127
+          const uint32_t need = top == 0 ? 0 : min(max((top >> 23) + 1u, 27u), 254u);
+          if (need > v_exp) {  // (all threads agree)
+            if (v_exp != 0) f *= exp2_fast((float)((int)v_exp - (int)need));
+            v_exp = need;
+          }
+          // 2^-(v_exp - 127); where every scale so far was zero it does not matter
+          inv_ref = __uint_as_float((v_exp == 254u ? 1u : 254u - max(v_exp, 27u)) << 23);
+          if (v_exp == 254u) inv_ref *= 0.5f;
+        }
+        if (i > (PAIR ? 0 : 1) && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t r16[16];
+            tmem_ld16(tO + c * 16, r16);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r16[e] = __float_as_uint(__uint_as_float(r16[e]) * f);
+            tmem_st16(tO + c * 16, r16);
+          }
+        }
+        const float neg = ref == -INFINITY ? 0.f : (E4M3 ? kShift - ref : -ref);
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), negx2 = f2_pack(neg, neg), invx2 = f2_pack(inv_ref, inv_ref);
+        uint64_t sum0 = 0, sum1 = 0;  // (pairs of float32 zeros)
+        const float* vsc = s_vsc + (tn + i) % kScales * kKeys;
+        // P goes out in two halves of the keys; O += P V starts on the first while the second is computed
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int c0 = hf * 64; c0 < (hf + 1) * 64; c0 += 32) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int c = c0 + 2 * e;
+              float p0, p1;
+              f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sl2x2, negx2), p0, p1);
+              p0 = exp2_fast(p0);
+              p1 = exp2_fast(p1);
+              const uint64_t p = f2_pack(p0, p1);
+              if (e & 1) sum1 = f2_add(sum1, p);
+              else sum0 = f2_add(sum0, p);
+              if constexpr (TOKEN) {
+                const float2 vs = *reinterpret_cast<const float2*>(vsc + c);
+                f2_unpack(f2_mul(f2_mul(p, f2_pack(vs.x, vs.y)), invx2), p0, p1);
+              }
+              hi[e] = pack2<E4M3>(p0, p1);
+              if (!E4M3) lo[e] = pack_rest(p0, p1, hi[e]);
+            }
+            if constexpr (E4M3) {
+              tmem_st16(tS + c0 / 2, hi);
+            } else {
+              tmem_st16(tS + hf * 64 + (c0 & 63) / 2, hi);
+              tmem_st16(tS + hf * 64 + 32 + (c0 & 63) / 2, lo);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_full + 2 * w + hf);
+        }
+        float a0, a1, a2, a3;
+        f2_unpack(sum0, a0, a1);
+        f2_unpack(sum1, a2, a3);
+        l += (a0 + a1) + (a2 + a3);
+      }
+      if (!ok) break;
+      if (TOKEN) v_mul = v_exp == 0 ? 0.f : __uint_as_float(v_exp << 23);
+      ok = mbar_wait<true>(o_full + w, (uint32_t)on & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+      if (!ok) break;
+      ++on;
+      tc_fence_after();
+
+      // ---- the segment's rows
+      const bool whole = sg.whole();
+      const long long part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
+      const bool odd = sg.t1 * kKeys > sg.base && (s_odd[segment % kFlags * 2] | s_odd[segment % kFlags * 2 + 1]) != 0;
+      auto store = [&](int d0, float* o) {  // columns d0 .. d0 + 31
+        if (!in) return;
+        if (odd) {
+#pragma unroll 1
+          for (int c = 0; c < 32; c += 4) {
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            add_odd_values<E4M3, TOKEN, D>(a, sg, tok, d0 + c, kKeys, acc);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              if (k == c) o[k] += acc.x, o[k + 1] += acc.y, o[k + 2] += acc.z, o[k + 3] += acc.w;
+          }
+        }
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.o + ((long long)(sg.off + tok) * a.Hq + sg.head * a.G + h) * D + d0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            dst[c] = make_uint4(pack2<false>(o[8 * c], o[8 * c + 1]), pack2<false>(o[8 * c + 2], o[8 * c + 3]),
+                                pack2<false>(o[8 * c + 4], o[8 * c + 5]), pack2<false>(o[8 * c + 6], o[8 * c + 7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + (part * a.rows + lr) * D + d0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+      };
+      auto store_lse = [&](float top, float sum) {
+        if (!in) return;
+        // the weights' factor (e4m3) comes off the logarithm
+        const float lse2 = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum) - (E4M3 ? kShift : 0.f);
+        if (!whole) a.part_lse[part * a.rows + lr] = lse2;
+        else if (a.lse)
+          a.lse[(long long)(sg.head * a.G + h) * g.total_tokens + sg.off + tok] = lse2 * 0.69314718055994531f;
+      };
+      if (PAIR || nt == 1) {
+        if (PAIR || w == 0) {
+          const float f = l == 0.f ? 0.f : v_mul / l;
+#pragma unroll 1
+          for (int d0 = 0; d0 < D; d0 += 32) {
+            uint32_t o[32];
+            float of[32];
+            tmem_ld32(tO + d0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) of[c] = f == 0.f ? 0.f : __uint_as_float(o[c]) * f;
+            store(d0, of);
+          }
+          store_lse(ref, l);
+        }
+      } else {
+        // the second warpgroup's part goes through Q's place (its products are over) in rounds of COLS columns
+        float* buf = reinterpret_cast<float*>(sQ);  // [COLS][128]
+        if (w == 1) s_half[row] = make_float4(ref, l, v_mul, 0.f);
+        float f0 = 0.f, f1 = 0.f, top = 0.f, sum = 0.f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += C::COLS) {
+          if (w == 1) {
+#pragma unroll 1
+            for (int d0 = 0; d0 < C::COLS; d0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c0 + d0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) buf[(d0 + c) * 128 + row] = __uint_as_float(o[c]);
+            }
+            mbar_arrive(half_full);
+          } else {
+            ok = mbar_wait<true>(half_full, (uint32_t)hn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+            if (!ok) break;
+            if (c0 == 0) {
+              const float4 y = s_half[row];
+              top = fmaxf(ref, y.x);
+              const float e0 = top == -INFINITY ? 1.f : exp2_fast(ref - top);
+              const float e1 = top == -INFINITY ? 1.f : exp2_fast(y.x - top);
+              sum = l * e0 + y.y * e1;
+              f0 = sum == 0.f ? 0.f : e0 * v_mul / sum;
+              f1 = sum == 0.f ? 0.f : e1 * y.z / sum;
+            }
+#pragma unroll 1
+            for (int d0 = 0; d0 < C::COLS; d0 += 32) {
+              uint32_t o[32];
+              float of[32];
+              tmem_ld32(tO + c0 + d0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const float y = buf[(d0 + c) * 128 + row];
+                of[c] = (f0 == 0.f ? 0.f : __uint_as_float(o[c]) * f0) + (f1 == 0.f ? 0.f : y * f1);
+              }
+              store(c0 + d0, of);
+            }
+            mbar_arrive(half_empty);
+          }
+          // both go on when the buffer is read: it is filled again, or with the next segment's Q
+          ok = mbar_wait<true>(half_empty, (uint32_t)hn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+          if (!ok) break;
+          ++hn;
+        }
+        if (!ok) break;
+        if (w == 0) store_lse(top, sum);
+      }
+      tc_fence_before();
+      base += 2 * nt;
+      tn += nt;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <bool E4M3, bool TOKEN, int D, bool PAIR>
+cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  using C = Cfg<E4M3, D, PAIR>;
+  auto kern = wide_kernel<E4M3, TOKEN, D, PAIR>;
+  // more than half of the SM's shared memory: one CTA per SM, so that the
+  // 512-column TMEM allocation never waits for a co-resident CTA
+  const int want = C::SMEM_FIXED + (a.g.R + 1) * 4, smem = want > 120 * 1024 ? want : 120 * 1024;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<a.grid, kThreads, smem, s>>>(mk, mv, a);
+  return cudaGetLastError();
+}
+
+template <bool E4M3, bool TOKEN, int D>
+cudaError_t run_rows(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  return a.rows > 128 ? run<E4M3, TOKEN, D, true>(a, mk, mv, s) : run<E4M3, TOKEN, D, false>(a, mk, mv, s);
+}
+
+}  // namespace
+
+cudaError_t launch_wide(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  if (a.g.e4m3) return a.g.token_scale ? run_rows<true, true, 128>(a, mk, mv, s) : run_rows<true, false, 128>(a, mk, mv, s);
+  return a.g.d == 128 ? run_rows<false, false, 128>(a, mk, mv, s) : run_rows<false, false, 64>(a, mk, mv, s);
+}
+
+}  // namespace tree
+}  // namespace fp
