@@ -11,13 +11,18 @@
 // own O, which meet at the segment's end: HBM, not the softmax of one
 // warpgroup, then bounds it.
 //
-// Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warp 8 TMA
-// producer, warp 9 MMA issuer, warps 10-11 converters. Operands are 16-bit:
-// bf16 caches multiply bf16 (P as hi + lo: two products, 16 bits of weight);
+// Roles (one CTA per SM): warps 0-3 and 4-7 softmax, warp 8 TMA producer, warps
+// 9 and 10 MMA issuers, one per softmax warpgroup (a lone issuer spent as long
+// waiting for either warpgroup's weights as the tensor cores worked: 206 us
+// where two take XXX), the last warps converters: one, or four for e4m3 caches (two widened a tile in 2800 clocks, which
+// set the pace). Operands are 16-bit:
+// bf16 caches multiply bf16, P rounded to bf16;
 // e4m3 caches are widened exactly to f16 by the converters, q goes to f16 as
 // q * 2^e with e per row such that max |q| lies in [2^14, 2^15), P to f16.
-// The converters also make the tiles that hold new tokens or end behind the
-// last one safe to multiply: V rows behind the last token become zeros, and so
+// The converters also pass every tile on in the order of its load (an issuer that
+// watched a slot of which the other one has the previous tile could take that
+// tile's phase for its own), and make those that hold new tokens or end behind
+// the last one safe to multiply: V rows behind the last token become zeros, and so
 // do infinities and NaN of new tokens, which only some rows see (those are
 // added to the rows that see them at the end).
 // Every wait is bounded; after one ran out every role leaves its loop, the MMA
@@ -34,14 +39,20 @@ namespace tree {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kConvertWarp = 10;
-// 2 x 128 x 200 + 128 x 104 = 384 x 168
-constexpr uint32_t kSoftmaxRegs = 200, kControlRegs = 104;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * 168, "register split exceeds the launch");
+constexpr int kProducerWarp = 8, kMmaWarp = 9;  // MMA issuers: kMmaWarp + softmax warpgroup
+template <bool E4M3>
+struct Roles {
+  static constexpr int THREADS = E4M3 ? 512 : 384;
+  static constexpr int CONVERT_WARP = E4M3 ? 12 : 11;
+  static constexpr int CONVERTERS = E4M3 ? 128 : 32;  // threads
+  // launched with 128 or 168 registers a thread: 2 x 128 x 176 + 256 x 80 = 512 x 128,
+  // 2 x 128 x 200 + 128 x 104 = 384 x 168
+  static constexpr uint32_t LAUNCH_REGS = E4M3 ? 128 : 168;
+  static constexpr uint32_t SOFTMAX_REGS = E4M3 ? 176 : 200, CONTROL_REGS = E4M3 ? 80 : 104;
+  static_assert(256 * SOFTMAX_REGS + (THREADS - 256) * CONTROL_REGS <= THREADS * LAUNCH_REGS, "register split");
+};
 constexpr int kKeys = 128;           // per tile
 constexpr int kChunk = kKeys * 128;  // bytes of a tile's 128-byte-wide chunk
-constexpr int kCleaned = 8;          // > V tiles that the ring can hold
 constexpr int kFlags = 8;            // > segments that the ring can reach into
 constexpr int kScales = 4;           // tiles whose token scales are kept (see the converters)
 
@@ -59,9 +70,9 @@ struct Cfg {
   static constexpr int AHEAD = PAIR ? 1 : 2;            // K tiles loaded before the first V tile
   static constexpr int LOAD_SLOTS = E4M3 ? RAW_SLOTS : SLOTS;
   static constexpr int LOAD_SLOT = E4M3 ? RAW_SLOT : TILE;
-  static constexpr int NUM_BARS = 2 * (SLOTS + RAW_SLOTS) + 2 + 2 + 4 + 2 + kCleaned + 3;
+  static constexpr int NUM_BARS = 2 * SLOTS + LOAD_SLOTS + RAW_SLOTS + 2 + 2 + 4 + 2 + 6;
   static constexpr int SMEM_FIXED = 1024 + Q + SLOTS * TILE + RAW_SLOTS * RAW_SLOT +
-                                    (E4M3 ? kScales * 2 * kKeys * 4 : 0) + 128 * 16 + NUM_BARS * 8 + 160;
+                                    (E4M3 ? kScales * 2 * kKeys * 4 : 0) + 128 * 16 + NUM_BARS * 8 + 320;
   static constexpr int COLS = Q / 512 < D ? Q / 512 : D;  // columns of O per round in which two warpgroups' O meet
   static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
   static_assert(COLS % 32 == 0 && D % COLS == 0, "rounds of whole TMEM loads");
@@ -100,9 +111,10 @@ template <bool PAIR>
 __device__ __forceinline__ int item_v(int i, int nt) { return PAIR ? 2 * i + 1 : min(2 * i + 2, 2 * nt - 1); }
 
 template <bool E4M3, bool TOKEN, int D, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
   using C = Cfg<E4M3, D, PAIR>;
+  using L = Roles<E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -113,46 +125,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   float4* s_half = reinterpret_cast<float4*>(s_vsc + (E4M3 ? kScales * kKeys : 0));  // [128] second warpgroup's ref, l, factor
   uint64_t* full = reinterpret_cast<uint64_t*>(s_half + 128);
   uint64_t* empty = full + C::SLOTS;
-  uint64_t* rfull = empty + C::SLOTS;
-  uint64_t* rempty = rfull + C::RAW_SLOTS;
+  uint64_t* loaded = empty + C::SLOTS;            // [LOAD_SLOTS]
+  uint64_t* rempty = loaded + C::LOAD_SLOTS;
   uint64_t* q_full = rempty + C::RAW_SLOTS;       // [2]
   uint64_t* s_full = q_full + 2;                  // [2]
   uint64_t* p_full = s_full + 2;                  // [warpgroup][half of the keys]
   uint64_t* o_full = p_full + 4;                  // [2]
-  uint64_t* cleaned = o_full + 2;                 // [kCleaned]: V tiles with new tokens or a ragged end, in turn
-  uint64_t* half_full = cleaned + kCleaned;
+  uint64_t* half_full = o_full + 2;
   uint64_t* half_empty = half_full + 1;
-  uint64_t* drain = half_empty + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = half_empty + 1;               // [2]
+  uint64_t* turn = drain + 2;                     // [2] (PAIR)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* warp_sum = reinterpret_cast<int*>(tmem_slot + 2);             // [12]
-  volatile uint32_t* s_vmax = tmem_slot + 14;                        // [kScales][2]
-  volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 22);  // [kFlags][2]
-  int* pre = reinterpret_cast<int*>(tmem_slot + 40);                 // [R + 1]
+  int* warp_sum = reinterpret_cast<int*>(tmem_slot + 2);             // [16]
+  volatile uint32_t* s_vmax = tmem_slot + 18;                        // [kScales][4]
+  volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 34);  // [kFlags][4]
+  int* pre = reinterpret_cast<int*>(tmem_slot + 66);                 // [R + 1]
 
   const CacheGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_init(full + s, E4M3 ? 64 : 1);
-      mbar_init(empty + s, 1);
+      mbar_init(full + s, L::CONVERTERS);
+      mbar_init(empty + s, PAIR ? 2 : 1);
     }
-    for (int s = 0; s < C::RAW_SLOTS; ++s) {
-      mbar_init(rfull + s, 1);
-      mbar_init(rempty + s, 64);
-    }
+    for (int s = 0; s < C::LOAD_SLOTS; ++s) mbar_init(loaded + s, 1);
+    for (int s = 0; s < C::RAW_SLOTS; ++s) mbar_init(rempty + s, L::CONVERTERS);
     for (int w = 0; w < 2; ++w) {
       mbar_init(q_full + w, PAIR ? 128 : 256);
       mbar_init(s_full + w, 1);
       mbar_init(p_full + 2 * w, 128);
       mbar_init(p_full + 2 * w + 1, 128);
-      mbar_init(o_full + w, 1);
+      mbar_init(o_full + w, PAIR ? 1 : 2);
+      mbar_init(drain + w, 1);
+      mbar_init(turn + w, 1);
     }
-    for (int k = 0; k < kCleaned; ++k) mbar_init(cleaned + k, 64);
     mbar_init(half_full, 128);
     mbar_init(half_empty, 128);
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -170,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (warp >= 8) reg_dealloc<kControlRegs>();
+  if (warp >= 8) reg_dealloc<L::CONTROL_REGS>();
 
   bool ok = true;
   int r = request_of(pre, g.R, x_begin);
@@ -180,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    uint64_t* lfull = E4M3 ? rfull : full;
     uint64_t* lempty = E4M3 ? rempty : empty;
     uint8_t* ring = E4M3 ? sR : sT;
     const int sub_rows = min(g.page_size, kKeys), sub_max = kKeys / sub_rows;  // sub_max <= 8
@@ -210,20 +219,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           uint32_t bytes = (uint32_t)(subs * sub_rows) * (D * C::ES);
           if (TOKEN) bytes += (uint32_t)(subs * sub_rows) * 4u;
-          mbar_arrive_expect_tx(lfull + slot, bytes);
+          mbar_arrive_expect_tx(loaded + slot, bytes);
         }
         __syncwarp();
         if (mine) {
           const int at = tok & (g.page_size - 1);
 #pragma unroll
           for (int ch = 0; ch < C::LOAD_CH; ++ch)
-            tma_load_4d(dst + ch * kChunk + lane * sub_rows * 128, v ? &tmV : &tmK, lfull + slot, ch * C::CH_ELEMS,
+            tma_load_4d(dst + ch * kChunk + lane * sub_rows * 128, v ? &tmV : &tmK, loaded + slot, ch * C::CH_ELEMS,
                         sg.head, at, page);
           if (TOKEN) {
             const float* sc = v ? g.v_scale : g.k_scale;
             const long long pg = bad ? 0 : page;  // (a bad page's codes are zeros: any scale does)
             bulk_load(dst + kChunk + lane * sub_rows * 4, sc + ((pg * g.Hkv + sg.head) << g.page_shift) + at,
-                      (uint32_t)sub_rows * 4u, lfull + slot);
+                      (uint32_t)sub_rows * 4u, loaded + slot);
           }
         }
         ++issued;
@@ -248,191 +257,156 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       for (int k = 0; k < min(issued, C::LOAD_SLOTS); ++k) {
         const int i = issued - 1 - k;
-        mbar_drain(lfull + i % C::LOAD_SLOTS, (uint32_t)((i / C::LOAD_SLOTS) & 1), g.status, FP_DEV_TIMEOUT);
+        mbar_drain(loaded + i % C::LOAD_SLOTS, (uint32_t)((i / C::LOAD_SLOTS) & 1), g.status, FP_DEV_TIMEOUT);
       }
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMA issuer
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // ------------------------------------------------------------------ MMA issuer of softmax warpgroup w
+    const int w = warp - kMmaWarp;
     if (lane == 0) {
       constexpr uint32_t fmt = E4M3 ? 0u : 1u;  // f16 or bf16
       const uint32_t idesc_qk = instr_desc(fmt, 128, kKeys, 0, 0);
       const uint32_t idesc_pv = instr_desc(fmt, 128, D, 0, 1);
-      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ) + (PAIR ? w : 0) * C::TILE, 16, 1024);
       const uint64_t dK = smem_desc_sw128(smem_u32(sT), 16, 1024);
       const uint64_t dV = smem_desc_sw128(smem_u32(sT), kChunk, 1024);
-      auto issue_qk = [&](int w, int slot) {
-        const uint64_t a0 = dQ + (uint64_t)(((PAIR ? w : 0) * C::TILE) >> 4);
+      const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
+      auto issue_qk = [&](int slot) {
         const uint64_t b0 = dK + (uint64_t)((slot * C::TILE) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (uint32_t)((ks >> 2) * kChunk + (ks & 3) * 32) >> 4;
-          umma_f16_ss(tmem + w * 128, a0 + off, b0 + off, idesc_qk, ks > 0);
+          umma_f16_ss(tS, dQ + off, b0 + off, idesc_qk, ks > 0);
         }
       };
-      // P of a half of the keys: f16, 32 columns; or bf16 hi, 32 columns, then lo, 32 columns
-      auto issue_pv = [&](int w, int slot, bool acc, int hf) {
+      // P of a half of the keys: 32 columns
+      auto issue_pv = [&](int slot, bool acc, int hf) {
         const uint64_t b0 = dV + (uint64_t)((slot * C::TILE) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kKeys / 32; ++ks) {
           const uint64_t bd = b0 + ((uint32_t)((hf * (kKeys / 32) + ks) * 16 * 128) >> 4);
-          const uint32_t pt = tmem + w * 128 + hf * (E4M3 ? 32 : 64) + ks * 8;
-          umma_f16_ts(tmem + 256 + w * 128, pt, bd, idesc_pv, (acc || ks > 0) ? 1u : 0u);
-          if (!E4M3) umma_f16_ts(tmem + 256 + w * 128, pt + 32, bd, idesc_pv, 1u);
+          umma_f16_ts(tO, tS + hf * 32 + ks * 8, bd, idesc_pv, (acc || ks > 0) ? 1u : 0u);
         }
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = mbar_wait(bar, parity, abort_flag, g.status, FP_DEV_TIMEOUT);
         return ok;
       };
-      int base = 0, qn = 0, cn = 0, pn[2] = {0, 0};
+      auto wait_item = [&](int item) { return wait(full + item % C::SLOTS, (uint32_t)(item / C::SLOTS) & 1u); };
+      int base = 0, qn = 0, pn = 0, turns = 0;
+      if (PAIR && w == 1) mbar_arrive(turn);  // the first turn is issuer 0's
       for (int x = x_begin; x < x_end && ok;) {
         const Segment sg = segment_at(a, pre, x, x_end, r);
         const int nt = sg.t1 - sg.t0;
         x += nt;
-        auto wait_item = [&](int item) { return wait(full + item % C::SLOTS, (uint32_t)(item / C::SLOTS) & 1u); };
-        if (!wait(q_full, (uint32_t)qn & 1u)) break;
-        if (PAIR && !wait(q_full + 1, (uint32_t)qn & 1u)) break;
+        const int first = PAIR ? 0 : w;                      // tiles first, first + AHEAD, ...
+        if (!wait(q_full + (PAIR ? w : 0), (uint32_t)qn & 1u)) break;
         ++qn;
-        if (!wait_item(base)) break;
-        tc_fence_after();
-        issue_qk(0, base % C::SLOTS);
-        umma_commit(s_full + 0);
-        if (PAIR) {
-          issue_qk(1, base % C::SLOTS);
-          umma_commit(s_full + 1);
-        }
-        umma_commit(empty + base % C::SLOTS);
-        if (!PAIR && nt > 1) {
-          const int item = base + 1;
+        if (first < nt) {
+          const int item = base + item_k<PAIR>(first);
           if (!wait_item(item)) break;
           tc_fence_after();
-          issue_qk(1, item % C::SLOTS);
-          umma_commit(s_full + 1);
+          issue_qk(item % C::SLOTS);
+          umma_commit(s_full + w);
           umma_commit(empty + item % C::SLOTS);
         }
-        for (int i = 0; i < nt; ++i) {
+        for (int i = first; i < nt; i += C::AHEAD) {
           const int vi = base + item_v<PAIR>(i, nt), vslot = vi % C::SLOTS;
-          if (!E4M3 && (sg.t0 + i + 1) * kKeys > sg.base) {  // cleaned after its copy landed
-            if (!wait(cleaned + cn % kCleaned, (uint32_t)(cn / kCleaned) & 1u)) break;
-            ++cn;
-          } else if (!wait_item(vi)) {
-            break;
-          }
           const bool more = i + C::AHEAD < nt;
           const int ki = base + item_k<PAIR>(i + C::AHEAD), kslot = ki % C::SLOTS;
-          bool k_there = !more;
-          const int w0 = PAIR ? 0 : i & 1, w1 = PAIR ? 1 : w0;
-#pragma unroll 1
-          for (int w = w0; w <= w1 && ok; ++w) {
-            const bool acc = PAIR ? i > 0 : i > 1;
-            if (!wait(p_full + 2 * w, (uint32_t)pn[w] & 1u)) break;
-            tc_fence_after();
-            issue_pv(w, vslot, acc, 0);
-            // the next K tile is waited for while the second half is computed
-            if (!k_there) {
-              if (!wait_item(ki)) break;
-              k_there = true;
-            }
-            if (!wait(p_full + 2 * w + 1, (uint32_t)pn[w] & 1u)) break;
-            ++pn[w];
-            tc_fence_after();
-            issue_pv(w, vslot, true, 1);
-            if (w == w1) umma_commit(empty + vslot);
-            if (more) {
-              issue_qk(w, kslot);
-              umma_commit(s_full + w);
-              if (w == w1) umma_commit(empty + kslot);
-            } else if (PAIR) {
-              umma_commit(o_full + w);
-            }
+          if (!wait_item(vi)) break;
+          if (PAIR && more && !wait_item(ki)) break;
+          if (!wait(p_full + 2 * w, (uint32_t)pn & 1u)) break;
+          // the issuers take turns, so that one M-tile's products run while the other's softmax does
+          if (PAIR && !wait(turn + w, (uint32_t)turns & 1u)) break;
+          ++turns;
+          tc_fence_after();
+          issue_pv(vslot, i > first, 0);
+          if (!PAIR && more && !wait_item(ki)) break;
+          if (!wait(p_full + 2 * w + 1, (uint32_t)pn & 1u)) break;
+          ++pn;
+          tc_fence_after();
+          issue_pv(vslot, true, 1);
+          if (more) {
+            issue_qk(kslot);
+            umma_commit(s_full + w);
           }
-          if (!ok) break;
+          if (PAIR) mbar_arrive(turn + (w ^ 1));
+          umma_commit(empty + vslot);
+          if (more) umma_commit(empty + kslot);
         }
         if (!ok) break;
-        if (!PAIR) {
-          umma_commit(o_full + 0);
-          umma_commit(o_full + 1);
-        }
+        umma_commit(o_full + w);
+        if (!PAIR) umma_commit(o_full + 1 - w);  // (a shared Q tile is free when both have done)
         base += 2 * nt;
       }
       // every MMA this thread issued has completed once `drain` flips
-      umma_commit(drain);
-      mbar_drain(drain, 0u, g.status, FP_DEV_TIMEOUT);
+      umma_commit(drain + w);
+      mbar_drain(drain + w, 0u, g.status, FP_DEV_TIMEOUT);
     }
-  } else if (warp >= kConvertWarp) {
+  } else if (warp >= L::CONVERT_WARP) {
     // ------------------------------------------------------------------ converters
-    const int ct = threadIdx.x - kConvertWarp * 32, cw = warp - kConvertWarp;
-    int base = 0, rn = 0, tn = 0, cn = 0, segment = 0;
+    const int ct = threadIdx.x - L::CONVERT_WARP * 32, cw = warp - L::CONVERT_WARP;
+    int base = 0, tn = 0, segment = 0;
     for (int x = x_begin; x < x_end && ok; ++segment) {
       const Segment sg = segment_at(a, pre, x, x_end, r);
       const int nt = sg.t1 - sg.t0;
       x += nt;
       bool fresh = true;  // the segment's flag is not cleared yet
       auto flag_odd = [&](bool odd) {
-        volatile int* f = s_odd + segment % kFlags * 2 + cw;
+        volatile int* f = s_odd + segment % kFlags * 4 + cw;
         if (fresh && lane == 0) *f = 0;
         fresh = false;
         __syncwarp();
         if (odd) *f = 1;
       };
-      if constexpr (!E4M3) {
-        for (int i = max(0, sg.base / kKeys - sg.t0); i < nt; ++i) {
-          const int vi = base + item_v<PAIR>(i, nt);
-          ok = mbar_wait<true>(full + vi % C::SLOTS, (uint32_t)(vi / C::SLOTS) & 1u, abort_flag, g.status,
-                               FP_DEV_TIMEOUT);
-          if (!ok) break;
-          uint8_t* tile = sT + (vi % C::SLOTS) * C::TILE;
-          bool odd = false;
-          for (int q = ct; q < C::CH * kKeys * 8; q += 64) {  // (where a granule lies in its row does not matter)
-            const int pos = (sg.t0 + i) * kKeys + ((q >> 3) & (kKeys - 1));
-            if (pos < sg.base) continue;
-            uint4* p = reinterpret_cast<uint4*>(tile) + q;
-            if (pos >= sg.kv) {
-              *p = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            const uint4 v = *p;
-            const uint32_t m = 0x7f807f80u;
-            const uint32_t b0 = __vcmpeq2(v.x & m, m), b1 = __vcmpeq2(v.y & m, m), b2 = __vcmpeq2(v.z & m, m),
-                           b3 = __vcmpeq2(v.w & m, m);
-            if (b0 | b1 | b2 | b3) {
-              odd = true;
-              *p = make_uint4(v.x & ~b0, v.y & ~b1, v.z & ~b2, v.w & ~b3);
-            }
-          }
-          flag_odd(odd);
-          fence_async();
-          mbar_arrive(cleaned + cn % kCleaned);
-          ++cn;
+      for (int item = 0; item < 2 * nt; ++item) {
+        // the item's kind and tile: item_k and item_v the other way round
+        bool v;
+        int i;
+        if (PAIR) {
+          v = item & 1;
+          i = item >> 1;
+        } else if (item < 2 || item == 2 * nt - 1) {
+          v = item == 2 * nt - 1;
+          i = v ? nt - 1 : item;
+        } else {
+          v = !(item & 1);
+          i = v ? item / 2 - 1 : (item + 1) / 2;
         }
-      } else {
-        for (int item = 0; item < 2 * nt && ok; ++item, ++rn) {
-          // the item's kind and tile: item_k and item_v the other way round
-          bool v;
-          int i;
-          if (PAIR) {
-            v = item & 1;
-            i = item >> 1;
-          } else if (item < 2 || item == 2 * nt - 1) {
-            v = item == 2 * nt - 1;
-            i = v ? nt - 1 : item;
-          } else {
-            v = !(item & 1);
-            i = v ? item / 2 - 1 : (item + 1) / 2;
+        const int n = base + item, ls = n % C::LOAD_SLOTS, ts = n % C::SLOTS;
+        ok = mbar_wait<true>(loaded + ls, (uint32_t)(n / C::LOAD_SLOTS) & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+        if (!ok) break;
+        const int pos0 = (sg.t0 + i) * kKeys;
+        const bool special = v && pos0 + kKeys > sg.base;
+        uint8_t* dst = sT + ts * C::TILE;
+        bool odd = false;
+        if constexpr (!E4M3) {
+          if (special) {
+            for (int q = ct; q < C::CH * kKeys * 8; q += L::CONVERTERS) {  // (where a granule lies in its row does not matter)
+              const int pos = pos0 + ((q >> 3) & (kKeys - 1));
+              if (pos < sg.base) continue;
+              uint4* p = reinterpret_cast<uint4*>(dst) + q;
+              if (pos >= sg.kv) {
+                *p = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              const uint4 w = *p;
+              const uint32_t m = 0x7f807f80u;
+              const uint32_t b0 = __vcmpeq2(w.x & m, m), b1 = __vcmpeq2(w.y & m, m), b2 = __vcmpeq2(w.z & m, m),
+                             b3 = __vcmpeq2(w.w & m, m);
+              if (b0 | b1 | b2 | b3) {
+                odd = true;
+                *p = make_uint4(w.x & ~b0, w.y & ~b1, w.z & ~b2, w.w & ~b3);
+              }
+            }
           }
-          const int rs = rn % C::RAW_SLOTS, ts = (base + item) % C::SLOTS;
-          ok = mbar_wait<true>(rfull + rs, (uint32_t)(rn / C::RAW_SLOTS) & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+        } else {
+          ok = mbar_wait<true>(empty + ts, ((uint32_t)(n / C::SLOTS) & 1u) ^ 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
           if (!ok) break;
-          ok = mbar_wait<true>(empty + ts, ((uint32_t)((base + item) / C::SLOTS) & 1u) ^ 1u, abort_flag, g.status,
-                               FP_DEV_TIMEOUT);
-          if (!ok) break;
-          const uint8_t* src = sR + rs * C::RAW_SLOT;
-          uint8_t* dst = sT + ts * C::TILE;
-          const int pos0 = (sg.t0 + i) * kKeys;
-          const bool special = v && pos0 + kKeys > sg.base;
-          bool odd = false;
+          const uint8_t* src = sR + ls * C::RAW_SLOT;
 #pragma unroll 4
-          for (int q = ct; q < kKeys * 8; q += 64) {
+          for (int q = ct; q < kKeys * 8; q += L::CONVERTERS) {
             const int key = q >> 3, g8 = q & 7, sw = key & 7;
             uint4 w = *reinterpret_cast<const uint4*>(src + key * 128 + ((g8 ^ sw) << 4));
             if (special && pos0 + key >= sg.base) {
@@ -454,39 +428,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Scales of the last kScales tiles: tile tn + i's are written when the slot of the
             // item three before its own is free, so the softmax of the tile four before it is over.
             const int at = (tn + i) % kScales;
-            float2 sc = *reinterpret_cast<const float2*>(src + kChunk + ct * 8);
+            float sc = *reinterpret_cast<const float*>(src + kChunk + ct * 4);  // (a converter per key)
             if (special) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& y = e ? sc.y : sc.x;
-                const int pos = pos0 + 2 * ct + e;
-                if (pos >= sg.kv) {
-                  y = 0.f;
-                } else if (pos >= sg.base && !(y < INFINITY)) {
-                  y = 0.f;
-                  odd = true;
-                }
+              const int pos = pos0 + ct;
+              if (pos >= sg.kv) {
+                sc = 0.f;
+              } else if (pos >= sg.base && !(sc < INFINITY)) {
+                sc = 0.f;
+                odd = true;
               }
             }
-            *reinterpret_cast<float2*>((v ? s_vsc : s_ksc) + at * kKeys + 2 * ct) = sc;
+            ((v ? s_vsc : s_ksc) + at * kKeys)[ct] = sc;
             if (v) {
               // (scales are not negative: they compare as integers)
-              const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(sc.x), __float_as_uint(sc.y)));
-              if (lane == 0) s_vmax[at * 2 + cw] = top;
+              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sc));
+              if (lane == 0) s_vmax[at * 4 + cw] = top;
             }
           }
-          if (special) flag_odd(odd);
-          fence_async();
-          mbar_arrive(full + ts);
-          mbar_arrive(rempty + rs);
         }
+        if (special) flag_odd(odd);
+        // the tensor cores read the tile through the async proxy
+        if (E4M3 || special) fence_async();
+        mbar_arrive(full + ts);
+        if (E4M3) mbar_arrive(rempty + ls);
       }
       base += 2 * nt;
       tn += nt;
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax warpgroups
-    reg_alloc<kSoftmaxRegs>();
+    reg_alloc<L::SOFTMAX_REGS>();
     const int w = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(row & ~31) << 16;
     const uint32_t tS = tmem + lane_base + w * 128;
@@ -550,7 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float v_mul = 1.f;  // what O is multiplied by at the end
       if (E4M3 && !TOKEN) v_mul = __ldg(g.v_scale + sg.head);
 
-      float ref = -INFINITY, l = 0.f;
+      // l: the sum of the weights; lu: of the weights as they are multiplied with V (bf16), by which O is
+      // divided, so that O stays an average of V rows whatever the rounding
+      float ref = -INFINITY, l = 0.f, lu = 0.f;
       uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
       for (int i = PAIR ? 0 : w; i < nt; i += PAIR ? 1 : 2) {
         ok = mbar_wait<true>(s_full + w, (uint32_t)sn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
@@ -605,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f = exp2_fast(ref - mx);
           ref = mx;
           l *= f;
+          lu *= f;
         }
         float inv_ref = 1.f;
         if constexpr (TOKEN) {
@@ -613,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                FP_DEV_TIMEOUT);
           if (!ok) break;
           const int at = (tn + i) % kScales;
-          const uint32_t top = max(s_vmax[at * 2], s_vmax[at * 2 + 1]);
+          const uint32_t top = max(max(s_vmax[at * 4], s_vmax[at * 4 + 1]), max(s_vmax[at * 4 + 2], s_vmax[at * 4 + 3]));
           // the next power of two above it, within 2^-100 .. 2^127
           const uint32_t need = top == 0 ? 0 : min(max((top >> 23) + 1u, 27u), 254u);
           if (need > v_exp) {  // (all threads agree)
@@ -637,14 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float neg = ref == -INFINITY ? 0.f : (E4M3 ? kShift - ref : -ref);
         const uint64_t sl2x2 = f2_pack(sl2, sl2), negx2 = f2_pack(neg, neg), invx2 = f2_pack(inv_ref, inv_ref);
-        uint64_t sum0 = 0, sum1 = 0;  // (pairs of float32 zeros)
+        uint64_t sum0 = 0, sum1 = 0, used0 = 0, used1 = 0;  // (pairs of float32 zeros)
         const float* vsc = s_vsc + (tn + i) % kScales * kKeys;
         // P goes out in two halves of the keys; O += P V starts on the first while the second is computed
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
           for (int c0 = hf * 64; c0 < (hf + 1) * 64; c0 += 32) {
-            uint32_t hi[16], lo[16];
+            uint32_t hi[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int c = c0 + 2 * e;
@@ -660,14 +634,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_unpack(f2_mul(f2_mul(p, f2_pack(vs.x, vs.y)), invx2), p0, p1);
               }
               hi[e] = pack2<E4M3>(p0, p1);
-              if (!E4M3) lo[e] = pack_rest(p0, p1, hi[e]);
+              if constexpr (!E4M3) {
+                const uint64_t q = f2_pack(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u));
+                if (e & 1) used1 = f2_add(used1, q);
+                else used0 = f2_add(used0, q);
+              }
             }
-            if constexpr (E4M3) {
-              tmem_st16(tS + c0 / 2, hi);
-            } else {
-              tmem_st16(tS + hf * 64 + (c0 & 63) / 2, hi);
-              tmem_st16(tS + hf * 64 + 32 + (c0 & 63) / 2, lo);
-            }
+            tmem_st16(tS + c0 / 2, hi);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -677,7 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         f2_unpack(sum0, a0, a1);
         f2_unpack(sum1, a2, a3);
         l += (a0 + a1) + (a2 + a3);
+        if constexpr (!E4M3) {
+          f2_unpack(used0, a0, a1);
+          f2_unpack(used1, a2, a3);
+          lu += (a0 + a1) + (a2 + a3);
+        }
       }
+      if (E4M3) lu = l;
       if (!ok) break;
       if (TOKEN) v_mul = v_exp == 0 ? 0.f : __uint_as_float(v_exp << 23);
       ok = mbar_wait<true>(o_full + w, (uint32_t)on & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
@@ -688,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the segment's rows
       const bool whole = sg.whole();
       const long long part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
-      const bool odd = sg.t1 * kKeys > sg.base && (s_odd[segment % kFlags * 2] | s_odd[segment % kFlags * 2 + 1]) != 0;
+      auto odd_values = [](volatile int* f) { return E4M3 ? (f[0] | f[1] | f[2] | f[3]) != 0 : f[0] != 0; };
+      const bool odd = sg.t1 * kKeys > sg.base && odd_values(s_odd + segment % kFlags * 4);
       auto store = [&](int d0, float* o) {  // columns d0 .. d0 + 31
         if (!in) return;
         if (odd) {
@@ -723,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (PAIR || nt == 1) {
         if (PAIR || w == 0) {
-          const float f = l == 0.f ? 0.f : v_mul / l;
+          const float f = lu == 0.f ? 0.f : v_mul / lu;
 #pragma unroll 1
           for (int d0 = 0; d0 < D; d0 += 32) {
             uint32_t o[32];
@@ -739,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // the second warpgroup's part goes through Q's place (its products are over) in rounds of COLS columns
         float* buf = reinterpret_cast<float*>(sQ);  // [COLS][128]
-        if (w == 1) s_half[row] = make_float4(ref, l, v_mul, 0.f);
+        if (w == 1) s_half[row] = make_float4(ref, l, v_mul, lu);
         float f0 = 0.f, f1 = 0.f, top = 0.f, sum = 0.f;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += C::COLS) {
@@ -762,8 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float e0 = top == -INFINITY ? 1.f : exp2_fast(ref - top);
               const float e1 = top == -INFINITY ? 1.f : exp2_fast(y.x - top);
               sum = l * e0 + y.y * e1;
-              f0 = sum == 0.f ? 0.f : e0 * v_mul / sum;
-              f1 = sum == 0.f ? 0.f : e1 * y.z / sum;
+              const float used = lu * e0 + y.w * e1;
+              f0 = used == 0.f ? 0.f : e0 * v_mul / used;
+              f1 = used == 0.f ? 0.f : e1 * y.z / used;
             }
 #pragma unroll 1
             for (int d0 = 0; d0 < C::COLS; d0 += 32) {
@@ -809,7 +790,7 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
   const int want = C::SMEM_FIXED + (a.g.R + 1) * 4, smem = want > 120 * 1024 ? want : 120 * 1024;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<a.grid, kThreads, smem, s>>>(mk, mv, a);
+  kern<<<a.grid, Roles<E4M3>::THREADS, smem, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 

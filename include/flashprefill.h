@@ -356,7 +356,9 @@ size_t fp_tree_workspace_size(const fp_cache_t* c, const fp_tree_t* t);
  * lse = -inf. Cached values at positions a row does not see, and slots at or
  * behind kv_lens[r], do not reach its result, whatever they hold (NaN and
  * infinities too). Scores, softmax sums and O are float32; the weights enter
- * O += P V as f16 (e4m3 caches), or as bf16 pairs hi + lo (bf16 caches).
+ * O += P V as f16 (e4m3 caches), or (bf16 caches) as bf16 pairs hi + lo, or, of
+ * requests with more than 16 rows (max_tokens * hq / hkv), as bf16, divided by
+ * the sum of the rounded weights.
  * The keys of all requests are divided evenly over the SMs; partial results
  * are combined in a fixed order, so equal calls give equal bits.
  * A request with n_r > max_tokens sets FP_DEV_BAD_SEQLENS and is skipped.

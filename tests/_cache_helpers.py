@@ -141,8 +141,10 @@ def check_tree(case, o, lse, scale=None):
     terms, the scalings and the subtraction of the maximum put the exponent off by at most
     (d + 8) 2^-23 A, the maximum's own error included by doubling; ex2.approx and its argument's
     rounding add 2^-21. So a weight is off by delta = 2 (d + 8) 2^-23 A + 2^-21 relative, before
-    it is rounded for the product with V: f16 (2^-11) for e4m3 caches, two bf16 (2^-16) otherwise,
-    and below f16's normal range by 2^-38 of the largest v. Sums over kv keys run in float32, in
+    it is rounded for the product with V: f16 (2^-11) for e4m3 caches, two bf16 (2^-16) otherwise up
+    to 16 rows, and below f16's normal range by 2^-38 of the largest v. Above 16 rows bf16 caches round
+    the weights to bf16, p (1 + e) with |e| <= 2^-8, and divide by the sum of the rounded ones:
+    O' - O = sum p e (v - O') / sum p, at most 2^-8 (W + |O'|) <= 2^-7 W. Sums over kv keys run in float32, in
     16-key products whose accumulation may truncate: (kv / 16 + 16) 2^-23. lse sees the weights'
     errors through their sum; O, a quotient, sees them twice, relative to W = sum p |v| / sum p;
     its own rounding to bf16 is 2^-8 |O|."""
@@ -153,7 +155,8 @@ def check_tree(case, o, lse, scale=None):
     o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
     kv = max(case.kv)
     delta = 2 * (case.d + 8) * 2.0 ** -23 * A + 2.0 ** -21 + (kv / 16 + 16) * 2.0 ** -23
-    p_round = 2.0 ** -16 if case.fmt == "bf16" else 2.0 ** -11
+    wide = max(case.n) * case.G > 16
+    p_round = 2.0 ** -11 if case.fmt != "bf16" else 2.0 ** -7 if wide else 2.0 ** -16
     vmax = np.nanmax(np.where(np.isfinite(W), W, 0)) if W.size else 0.0
     tol = 2.0 ** -8 * np.abs(O) + (2 * delta + p_round)[..., None] * W * 1.01 + kv * 2.0 ** -38 * vmax * 64
     finite = np.isfinite(O)
