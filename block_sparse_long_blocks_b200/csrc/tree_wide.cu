@@ -12,21 +12,26 @@
 // warpgroup, then bounds it.
 //
 // Roles (one CTA per SM): warps 0-3 and 4-7 softmax, warp 8 TMA producer, warps
-// 9 and 10 MMA issuers, one per softmax warpgroup (a lone issuer spent as long
-// waiting for either warpgroup's weights as the tensor cores worked: 206 us
-// where two take XXX), the last warps converters: one, or four for e4m3 caches (two widened a tile in 2800 clocks, which
-// set the pace). Operands are 16-bit:
-// bf16 caches multiply bf16, P rounded to bf16;
-// e4m3 caches are widened exactly to f16 by the converters, q goes to f16 as
-// q * 2^e with e per row such that max |q| lies in [2^14, 2^15), P to f16.
-// The converters also pass every tile on in the order of its load (an issuer that
-// watched a slot of which the other one has the previous tile could take that
-// tile's phase for its own), and make those that hold new tokens or end behind
-// the last one safe to multiply: V rows behind the last token become zeros, and so
-// do infinities and NaN of new tokens, which only some rows see (those are
-// added to the rows that see them at the end).
+// 9 and 10 MMA issuers, one per softmax warpgroup, the last warps converters.
+// PAIR: the issuers take turns, which keeps one M-tile's products under the
+// other's softmax; untied, both warpgroups fell into step, softmax and products
+// one after the other (64-token tree over 128K keys: 234 us untied, 206 us with
+// one issuer that waits for either warpgroup in turn, 191 us with turns).
+// Operands: bf16 caches multiply bf16, with P rounded to bf16 (as hi + lo, 191
+// us, otherwise 165). e4m3 caches: S on the e4m3 path with q * 2^e (e per row
+// such that max |q| lies in [2^7, 2^8)) as the sum hi + lo of two e4m3 values,
+// exact for elements within 2^-10 of the row's largest, others to 2^-18 of it;
+// the two products take the time of one on 16-bit operands, and K is multiplied
+// as it was loaded. V is widened exactly to f16 by the converters, P goes to f16.
+// The converters also pass the V tiles on in order, and make those that hold new
+// tokens or end behind the last one safe to multiply: rows behind the last token
+// become zeros, and so do infinities and NaN of new tokens, which only some rows
+// see (those are added to the rows that see them at the end).
+// An issuer may watch the phase of a slot only if it has seen all earlier ones
+// of that slot: key tiles alternate between the warpgroups over all segments,
+// and the K ring has an even number of slots, so a slot is always of one issuer.
 // Every wait is bounded; after one ran out every role leaves its loop, the MMA
-// issuer and the producer wait for what they have in flight, outputs are
+// issuers and the producer wait for what they have in flight, outputs are
 // invalid and FP_DEV_TIMEOUT is set.
 #include <cuda.h>
 
@@ -54,27 +59,31 @@ struct Roles {
 constexpr int kKeys = 128;           // per tile
 constexpr int kChunk = kKeys * 128;  // bytes of a tile's 128-byte-wide chunk
 constexpr int kFlags = 8;            // > segments that the ring can reach into
-constexpr int kScales = 4;           // tiles whose token scales are kept (see the converters)
+constexpr int kScales = 8;           // tiles whose token scales are kept (see the producer)
 
 template <bool E4M3, int D, bool PAIR>
 struct Cfg {
   static constexpr int ES = E4M3 ? 1 : 2;
   static constexpr int CH = D / 64;                     // chunks of a 16-bit tile
-  static constexpr int TILE = CH * kChunk;              // bytes of a 16-bit K, V or Q tile
+  static constexpr int TILE = CH * kChunk;              // bytes of a 16-bit tile
   static constexpr int LOAD_CH = D * ES / 128;          // chunks of a loaded tile
+  static constexpr int LOAD = LOAD_CH * kChunk;         // bytes of a loaded tile
   static constexpr int CH_ELEMS = 128 / ES;
-  static constexpr int Q = (PAIR ? 2 : 1) * TILE;
-  static constexpr int SLOTS = E4M3 ? 3 : D == 64 ? 8 : PAIR ? 4 : 5;   // 16-bit tiles
-  static constexpr int RAW_SLOTS = E4M3 ? (PAIR ? 2 : 4) : 0;           // e4m3 tiles as loaded, + their scales
-  static constexpr int RAW_SLOT = kChunk + 1024;
-  static constexpr int AHEAD = PAIR ? 1 : 2;            // K tiles loaded before the first V tile
-  static constexpr int LOAD_SLOTS = E4M3 ? RAW_SLOTS : SLOTS;
-  static constexpr int LOAD_SLOT = E4M3 ? RAW_SLOT : TILE;
-  static constexpr int NUM_BARS = 2 * SLOTS + LOAD_SLOTS + RAW_SLOTS + 2 + 2 + 4 + 2 + 6;
-  static constexpr int SMEM_FIXED = 1024 + Q + SLOTS * TILE + RAW_SLOTS * RAW_SLOT +
-                                    (E4M3 ? kScales * 2 * kKeys * 4 : 0) + 128 * 16 + NUM_BARS * 8 + 320;
+  static constexpr int Q1 = E4M3 ? 2 * kChunk : TILE;   // one M-tile's Q (e4m3: hi, then lo)
+  static constexpr int Q = (PAIR ? 2 : 1) * Q1;
+  // slots: K and V tiles as loaded, and (e4m3) V tiles as f16
+  static constexpr int K_SLOTS = D == 64 ? 4 : E4M3 && !PAIR ? 4 : 2;
+  static constexpr int V_SLOTS = D == 64 ? 4 : !E4M3 && !PAIR ? 3 : 2;
+  static constexpr int W_SLOTS = E4M3 ? 2 : 0;
+  static constexpr int M_SLOTS = E4M3 ? W_SLOTS : V_SLOTS;  // V tiles as multiplied
+  static constexpr int AHEAD = PAIR ? 1 : 2;            // K tiles loaded before the first V tile; tiles from one
+                                                        // of a warpgroup to its next
+  static constexpr int NUM_BARS = 2 * K_SLOTS + 2 * V_SLOTS + 2 * M_SLOTS + 2 + 2 + 4 + 2 + 6;
+  static constexpr int SMEM_FIXED = 1024 + Q + (K_SLOTS + V_SLOTS) * LOAD + W_SLOTS * TILE +
+                                    (E4M3 ? kScales * 2 * kKeys * 4 : 0) + 128 * 16 + NUM_BARS * 8 + 336;
   static constexpr int COLS = Q / 512 < D ? Q / 512 : D;  // columns of O per round in which two warpgroups' O meet
   static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
+  static_assert(K_SLOTS % 2 == 0, "a slot is of one issuer");
   static_assert(COLS % 32 == 0 && D % COLS == 0, "rounds of whole TMEM loads");
 };
 
@@ -103,13 +112,6 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Where a segment's tiles lie in the sequence of ring items (K and V tiles).
-// PAIR: K0 V0 K1 V1 ...; otherwise one more K tile goes ahead: K0 K1 V0 K2 V1 ...
-template <bool PAIR>
-__device__ __forceinline__ int item_k(int i) { return PAIR ? 2 * i : max(0, 2 * i - 1); }
-template <bool PAIR>
-__device__ __forceinline__ int item_v(int i, int nt) { return PAIR ? 2 * i + 1 : min(2 * i + 2, 2 * nt - 1); }
-
 template <bool E4M3, bool TOKEN, int D, bool PAIR>
 __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
@@ -118,16 +120,20 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sT = sQ + C::Q;                        // 16-bit tiles
-  uint8_t* sR = sT + C::SLOTS * C::TILE;          // e4m3 tiles as loaded
-  float* s_ksc = reinterpret_cast<float*>(sR + C::RAW_SLOTS * C::RAW_SLOT);  // [kScales][kKeys]
+  uint8_t* sK = sQ + C::Q;
+  uint8_t* sV = sK + C::K_SLOTS * C::LOAD;
+  uint8_t* sW = sV + C::V_SLOTS * C::LOAD;       // f16 V tiles (e4m3)
+  uint8_t* sM = E4M3 ? sW : sV;                  // V tiles as multiplied
+  float* s_ksc = reinterpret_cast<float*>(sW + C::W_SLOTS * C::TILE);  // [kScales][kKeys]
   float* s_vsc = s_ksc + (E4M3 ? kScales * kKeys : 0);
-  float4* s_half = reinterpret_cast<float4*>(s_vsc + (E4M3 ? kScales * kKeys : 0));  // [128] second warpgroup's ref, l, factor
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_half + 128);
-  uint64_t* empty = full + C::SLOTS;
-  uint64_t* loaded = empty + C::SLOTS;            // [LOAD_SLOTS]
-  uint64_t* rempty = loaded + C::LOAD_SLOTS;
-  uint64_t* q_full = rempty + C::RAW_SLOTS;       // [2]
+  float4* s_half = reinterpret_cast<float4*>(s_vsc + (E4M3 ? kScales * kKeys : 0));  // [128] second warpgroup's sums
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(s_half + 128);
+  uint64_t* k_empty = k_full + C::K_SLOTS;
+  uint64_t* v_full = k_empty + C::K_SLOTS;        // loaded
+  uint64_t* v_empty = v_full + C::V_SLOTS;
+  uint64_t* m_full = v_empty + C::V_SLOTS;        // ready to be multiplied
+  uint64_t* m_empty = m_full + C::M_SLOTS;        // (bf16: the loaded tiles themselves, v_empty)
+  uint64_t* q_full = m_empty + C::M_SLOTS;        // [2]
   uint64_t* s_full = q_full + 2;                  // [2]
   uint64_t* p_full = s_full + 2;                  // [warpgroup][half of the keys]
   uint64_t* o_full = p_full + 4;                  // [2]
@@ -139,19 +145,26 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* warp_sum = reinterpret_cast<int*>(tmem_slot + 2);             // [16]
   volatile uint32_t* s_vmax = tmem_slot + 18;                        // [kScales][4]
-  volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 34);  // [kFlags][4]
-  int* pre = reinterpret_cast<int*>(tmem_slot + 66);                 // [R + 1]
+  volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 50);  // [kFlags][4]
+  int* pre = reinterpret_cast<int*>(tmem_slot + 82);                 // [R + 1]
 
   const CacheGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_init(full + s, L::CONVERTERS);
-      mbar_init(empty + s, PAIR ? 2 : 1);
+    constexpr uint32_t issuers = PAIR ? 2 : 1;  // that multiply with a tile
+    for (int s = 0; s < C::K_SLOTS; ++s) {
+      mbar_init(k_full + s, 1);
+      mbar_init(k_empty + s, issuers);
     }
-    for (int s = 0; s < C::LOAD_SLOTS; ++s) mbar_init(loaded + s, 1);
-    for (int s = 0; s < C::RAW_SLOTS; ++s) mbar_init(rempty + s, L::CONVERTERS);
+    for (int s = 0; s < C::V_SLOTS; ++s) {
+      mbar_init(v_full + s, 1);
+      mbar_init(v_empty + s, E4M3 ? L::CONVERTERS : issuers);
+    }
+    for (int s = 0; s < C::M_SLOTS; ++s) {
+      mbar_init(m_full + s, L::CONVERTERS);
+      mbar_init(m_empty + s, issuers);
+    }
     for (int w = 0; w < 2; ++w) {
       mbar_init(q_full + w, PAIR ? 128 : 256);
       mbar_init(s_full + w, 1);
@@ -190,11 +203,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    uint64_t* lempty = E4M3 ? rempty : empty;
-    uint8_t* ring = E4M3 ? sR : sT;
     const int sub_rows = min(g.page_size, kKeys), sub_max = kKeys / sub_rows;  // sub_max <= 8
-    int slot = 0, issued = 0;
-    uint32_t phase = 0;
+    int kn = 0, vn = 0;  // K and V tiles issued
     for (int x = x_begin; x < x_end && ok;) {
       const Segment sg = segment_at(a, pre, x, x_end, r);
       const int nt = sg.t1 - sg.t0;
@@ -204,6 +214,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
         const int tok = (sg.t0 + i) * kKeys + lane * sub_rows;
         return (i < nt && lane < sub_max && tok < sg.kv) ? __ldg(row + (tok >> g.page_shift)) : -1;
       };
+      // Token scales go to rings of kScales tiles. Tile n's replace those of n - 8, whose softmax is over: K n waits
+      // for the product with K n - 2 or n - 4 and so for the softmax of n - 3 or n - 6 (of its warpgroup), V n for
+      // the conversion of V n - 2 and so for the product with V n - 4.
       auto load = [&](bool v, int i, int page) {
         const int tok = (sg.t0 + i) * kKeys + lane * sub_rows;
         const bool mine = lane < sub_max && tok < sg.kv;
@@ -213,33 +226,33 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           atomicOr(g.status, FP_DEV_BAD_PAGE);
           page = g.num_pages;  // outside the pool: the copy fills zeros
         }
-        ok = mbar_wait<true>(lempty + slot, phase ^ 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+        const int n = v ? vn : kn, slots = v ? C::V_SLOTS : C::K_SLOTS, slot = n % slots;
+        uint64_t* bar = (v ? v_full : k_full) + slot;
+        ok = mbar_wait<true>((v ? v_empty : k_empty) + slot, ((uint32_t)(n / slots) & 1u) ^ 1u, abort_flag, g.status,
+                             FP_DEV_TIMEOUT);
         if (!ok) return;
-        uint8_t* dst = ring + slot * C::LOAD_SLOT;
+        uint8_t* dst = (v ? sV : sK) + slot * C::LOAD;
         if (lane == 0) {
           uint32_t bytes = (uint32_t)(subs * sub_rows) * (D * C::ES);
           if (TOKEN) bytes += (uint32_t)(subs * sub_rows) * 4u;
-          mbar_arrive_expect_tx(loaded + slot, bytes);
+          mbar_arrive_expect_tx(bar, bytes);
         }
         __syncwarp();
         if (mine) {
           const int at = tok & (g.page_size - 1);
 #pragma unroll
           for (int ch = 0; ch < C::LOAD_CH; ++ch)
-            tma_load_4d(dst + ch * kChunk + lane * sub_rows * 128, v ? &tmV : &tmK, loaded + slot, ch * C::CH_ELEMS,
-                        sg.head, at, page);
+            tma_load_4d(dst + ch * kChunk + lane * sub_rows * 128, v ? &tmV : &tmK, bar, ch * C::CH_ELEMS, sg.head, at,
+                        page);
           if (TOKEN) {
-            const float* sc = v ? g.v_scale : g.k_scale;
             const long long pg = bad ? 0 : page;  // (a bad page's codes are zeros: any scale does)
-            bulk_load(dst + kChunk + lane * sub_rows * 4, sc + ((pg * g.Hkv + sg.head) << g.page_shift) + at,
-                      (uint32_t)sub_rows * 4u, loaded + slot);
+            bulk_load((v ? s_vsc : s_ksc) + n % kScales * kKeys + lane * sub_rows,
+                      (v ? g.v_scale : g.k_scale) + ((pg * g.Hkv + sg.head) << g.page_shift) + at,
+                      (uint32_t)sub_rows * 4u, bar);
           }
         }
-        ++issued;
-        if (++slot == C::LOAD_SLOTS) {
-          slot = 0;
-          phase ^= 1u;
-        }
+        if (v) ++vn;
+        else ++kn;
       };
       int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2);
       load(false, 0, p0);
@@ -255,28 +268,35 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     }
     // every copy lands before the CTA's shared memory is released
     if (lane == 0) {
-      for (int k = 0; k < min(issued, C::LOAD_SLOTS); ++k) {
-        const int i = issued - 1 - k;
-        mbar_drain(loaded + i % C::LOAD_SLOTS, (uint32_t)((i / C::LOAD_SLOTS) & 1), g.status, FP_DEV_TIMEOUT);
-      }
+      for (int k = max(0, kn - C::K_SLOTS); k < kn; ++k)
+        mbar_drain(k_full + k % C::K_SLOTS, (uint32_t)(k / C::K_SLOTS) & 1u, g.status, FP_DEV_TIMEOUT);
+      for (int k = max(0, vn - C::V_SLOTS); k < vn; ++k)
+        mbar_drain(v_full + k % C::V_SLOTS, (uint32_t)(k / C::V_SLOTS) & 1u, g.status, FP_DEV_TIMEOUT);
     }
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------ MMA issuer of softmax warpgroup w
     const int w = warp - kMmaWarp;
     if (lane == 0) {
-      constexpr uint32_t fmt = E4M3 ? 0u : 1u;  // f16 or bf16
-      const uint32_t idesc_qk = instr_desc(fmt, 128, kKeys, 0, 0);
-      const uint32_t idesc_pv = instr_desc(fmt, 128, D, 0, 1);
-      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ) + (PAIR ? w : 0) * C::TILE, 16, 1024);
-      const uint64_t dK = smem_desc_sw128(smem_u32(sT), 16, 1024);
-      const uint64_t dV = smem_desc_sw128(smem_u32(sT), kChunk, 1024);
+      // S: e4m3 or bf16; O += P V: f16 or bf16
+      constexpr uint32_t idesc_qk = instr_desc(E4M3 ? 0u : 1u, 128, kKeys, 0, 0);
+      constexpr uint32_t idesc_pv = instr_desc(E4M3 ? 0u : 1u, 128, D, 0, 1);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ) + (PAIR ? w : 0) * C::Q1, 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(sM), kChunk, 1024);
       const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
       auto issue_qk = [&](int slot) {
-        const uint64_t b0 = dK + (uint64_t)((slot * C::TILE) >> 4);
+        const uint64_t b0 = dK + (uint64_t)((slot * C::LOAD) >> 4);
+        if constexpr (E4M3) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (uint32_t)((ks >> 2) * kChunk + (ks & 3) * 32) >> 4;
-          umma_f16_ss(tS, dQ + off, b0 + off, idesc_qk, ks > 0);
+          for (int ks = 0; ks < 2 * D / 32; ++ks)  // hi, then lo
+            umma_f8_ss(tS, dQ + (uint32_t)(((ks >> 2) * kChunk + (ks & 3) * 32) >> 4), b0 + (uint32_t)(((ks & 3) * 32) >> 4),
+                       idesc_qk, ks > 0);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (uint32_t)((ks >> 2) * kChunk + (ks & 3) * 32) >> 4;
+            umma_f16_ss(tS, dQ + off, b0 + off, idesc_qk, ks > 0);
+          }
         }
       };
       // P of a half of the keys: 32 columns
@@ -292,37 +312,37 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
         ok = mbar_wait(bar, parity, abort_flag, g.status, FP_DEV_TIMEOUT);
         return ok;
       };
-      auto wait_item = [&](int item) { return wait(full + item % C::SLOTS, (uint32_t)(item / C::SLOTS) & 1u); };
-      int base = 0, qn = 0, pn = 0, turns = 0;
+      auto wait_k = [&](int n) { return wait(k_full + n % C::K_SLOTS, (uint32_t)(n / C::K_SLOTS) & 1u); };
+      auto wait_v = [&](int n) { return wait(m_full + n % C::M_SLOTS, (uint32_t)(n / C::M_SLOTS) & 1u); };
+      uint64_t* v_done = E4M3 ? m_empty : v_empty;
+      int tn = 0, qn = 0, pn = 0, turns = 0;
       if (PAIR && w == 1) mbar_arrive(turn);  // the first turn is issuer 0's
       for (int x = x_begin; x < x_end && ok;) {
         const Segment sg = segment_at(a, pre, x, x_end, r);
         const int nt = sg.t1 - sg.t0;
         x += nt;
-        const int first = PAIR ? 0 : w;                      // tiles first, first + AHEAD, ...
+        const int first = PAIR ? 0 : (w - tn) & 1;  // tiles first, first + AHEAD, ...
         if (!wait(q_full + (PAIR ? w : 0), (uint32_t)qn & 1u)) break;
         ++qn;
         if (first < nt) {
-          const int item = base + item_k<PAIR>(first);
-          if (!wait_item(item)) break;
+          const int n = tn + first;
+          if (!wait_k(n)) break;
           tc_fence_after();
-          issue_qk(item % C::SLOTS);
+          issue_qk(n % C::K_SLOTS);
           umma_commit(s_full + w);
-          umma_commit(empty + item % C::SLOTS);
+          umma_commit(k_empty + n % C::K_SLOTS);
         }
         for (int i = first; i < nt; i += C::AHEAD) {
-          const int vi = base + item_v<PAIR>(i, nt), vslot = vi % C::SLOTS;
           const bool more = i + C::AHEAD < nt;
-          const int ki = base + item_k<PAIR>(i + C::AHEAD), kslot = ki % C::SLOTS;
-          if (!wait_item(vi)) break;
-          if (PAIR && more && !wait_item(ki)) break;
+          const int v = tn + i, vslot = v % C::M_SLOTS, k = v + C::AHEAD, kslot = k % C::K_SLOTS;
+          if (!wait_v(v)) break;
+          if (PAIR && more && !wait_k(k)) break;
           if (!wait(p_full + 2 * w, (uint32_t)pn & 1u)) break;
-          // the issuers take turns, so that one M-tile's products run while the other's softmax does
           if (PAIR && !wait(turn + w, (uint32_t)turns & 1u)) break;
           ++turns;
           tc_fence_after();
           issue_pv(vslot, i > first, 0);
-          if (!PAIR && more && !wait_item(ki)) break;
+          if (!PAIR && more && !wait_k(k)) break;
           if (!wait(p_full + 2 * w + 1, (uint32_t)pn & 1u)) break;
           ++pn;
           tc_fence_after();
@@ -332,13 +352,13 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             umma_commit(s_full + w);
           }
           if (PAIR) mbar_arrive(turn + (w ^ 1));
-          umma_commit(empty + vslot);
-          if (more) umma_commit(empty + kslot);
+          umma_commit(v_done + vslot);
+          if (more) umma_commit(k_empty + kslot);
         }
         if (!ok) break;
         umma_commit(o_full + w);
         if (!PAIR) umma_commit(o_full + 1 - w);  // (a shared Q tile is free when both have done)
-        base += 2 * nt;
+        tn += nt;
       }
       // every MMA this thread issued has completed once `drain` flips
       umma_commit(drain + w);
@@ -347,7 +367,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   } else if (warp >= L::CONVERT_WARP) {
     // ------------------------------------------------------------------ converters
     const int ct = threadIdx.x - L::CONVERT_WARP * 32, cw = warp - L::CONVERT_WARP;
-    int base = 0, tn = 0, segment = 0;
+    int tn = 0, segment = 0;
     for (int x = x_begin; x < x_end && ok; ++segment) {
       const Segment sg = segment_at(a, pre, x, x_end, r);
       const int nt = sg.t1 - sg.t0;
@@ -360,26 +380,13 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
         __syncwarp();
         if (odd) *f = 1;
       };
-      for (int item = 0; item < 2 * nt; ++item) {
-        // the item's kind and tile: item_k and item_v the other way round
-        bool v;
-        int i;
-        if (PAIR) {
-          v = item & 1;
-          i = item >> 1;
-        } else if (item < 2 || item == 2 * nt - 1) {
-          v = item == 2 * nt - 1;
-          i = v ? nt - 1 : item;
-        } else {
-          v = !(item & 1);
-          i = v ? item / 2 - 1 : (item + 1) / 2;
-        }
-        const int n = base + item, ls = n % C::LOAD_SLOTS, ts = n % C::SLOTS;
-        ok = mbar_wait<true>(loaded + ls, (uint32_t)(n / C::LOAD_SLOTS) & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+      for (int i = 0; i < nt; ++i, ++tn) {
+        const int vs = tn % C::V_SLOTS, ms = tn % C::M_SLOTS;
+        ok = mbar_wait<true>(v_full + vs, (uint32_t)(tn / C::V_SLOTS) & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
         if (!ok) break;
         const int pos0 = (sg.t0 + i) * kKeys;
-        const bool special = v && pos0 + kKeys > sg.base;
-        uint8_t* dst = sT + ts * C::TILE;
+        const bool special = pos0 + kKeys > sg.base;
+        uint8_t* dst = sM + ms * C::TILE;
         bool odd = false;
         if constexpr (!E4M3) {
           if (special) {
@@ -402,10 +409,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             }
           }
         } else {
-          ok = mbar_wait<true>(empty + ts, ((uint32_t)(n / C::SLOTS) & 1u) ^ 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+          ok = mbar_wait<true>(m_empty + ms, ((uint32_t)(tn / C::M_SLOTS) & 1u) ^ 1u, abort_flag, g.status,
+                               FP_DEV_TIMEOUT);
           if (!ok) break;
-          const uint8_t* src = sR + ls * C::RAW_SLOT;
-#pragma unroll 4
+          const uint8_t* src = sV + vs * C::LOAD;
+#pragma unroll
           for (int q = ct; q < kKeys * 8; q += L::CONVERTERS) {
             const int key = q >> 3, g8 = q & 7, sw = key & 7;
             uint4 w = *reinterpret_cast<const uint4*>(src + key * 128 + ((g8 ^ sw) << 4));
@@ -425,10 +433,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
                 make_uint4(widen_lo(w.z), widen_hi(w.z), widen_lo(w.w), widen_hi(w.w));
           }
           if constexpr (TOKEN) {
-            // Scales of the last kScales tiles: tile tn + i's are written when the slot of the
-            // item three before its own is free, so the softmax of the tile four before it is over.
-            const int at = (tn + i) % kScales;
-            float sc = *reinterpret_cast<const float*>(src + kChunk + ct * 4);  // (a converter per key)
+            float& at = s_vsc[tn % kScales * kKeys + ct];  // (a converter per key)
+            float sc = at;
             if (special) {
               const int pos = pos0 + ct;
               if (pos >= sg.kv) {
@@ -437,23 +443,19 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
                 sc = 0.f;
                 odd = true;
               }
+              at = sc;
             }
-            ((v ? s_vsc : s_ksc) + at * kKeys)[ct] = sc;
-            if (v) {
-              // (scales are not negative: they compare as integers)
-              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sc));
-              if (lane == 0) s_vmax[at * 4 + cw] = top;
-            }
+            // (scales are not negative: they compare as integers)
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sc));
+            if (lane == 0) s_vmax[tn % kScales * 4 + cw] = top;
           }
         }
         if (special) flag_odd(odd);
         // the tensor cores read the tile through the async proxy
         if (E4M3 || special) fence_async();
-        mbar_arrive(full + ts);
-        if (E4M3) mbar_arrive(rempty + ls);
+        mbar_arrive(m_full + ms);
+        if (E4M3) mbar_arrive(v_empty + vs);
       }
-      base += 2 * nt;
-      tn += nt;
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax warpgroups
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     const uint32_t lane_base = (uint32_t)(row & ~31) << 16;
     const uint32_t tS = tmem + lane_base + w * 128;
     const uint32_t tO = tmem + lane_base + 256 + w * 128;
-    int base = 0, tn = 0, sn = 0, on = 0, hn = 0, segment = 0;
+    int tn = 0, sn = 0, on = 0, hn = 0, segment = 0;
     for (int x = x_begin; x < x_end; ++segment) {
       const Segment sg = segment_at(a, pre, x, x_end, r);
       const int nt = sg.t1 - sg.t0;
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       {
         const uint4* qp = reinterpret_cast<const uint4*>(a.q + (long long)(sg.off + tok) * a.q_stride +
                                                          (sg.head * a.G + h) * D);
-        uint8_t* dst = sQ + (PAIR ? w * C::TILE : 0) + row * 128;
+        uint8_t* dst = sQ + (PAIR ? w * C::Q1 : 0) + row * 128;
         if constexpr (!E4M3) {
 #pragma unroll
           for (int ch = 0; ch < C::CH; ++ch) {
@@ -496,23 +498,31 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             for (int e = 0; e < 4; ++e)
               mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
           }
-          // times 2^(14 - floor(log2 max)); rows of zeros, infinities or below 2^-100 take the limits
-          int e2 = (int)((__float_as_uint(mx) >> 23) & 255u) - 127;
-          e2 = mx == 0.f || e2 > 127 ? 14 : max(e2, -100);
-          const float up = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
-          sl2 *= __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+          // times 2^(7 - floor(log2 max)): the largest lies in [2^7, 2^8); rows of zeros or below 2^-100 take the limits
+          const int e2 = mx == 0.f ? 7 : max((int)((__float_as_uint(mx) >> 23) & 255u) - 127, -100);
+          const float up = mx < INFINITY ? __uint_as_float((uint32_t)(7 - e2 + 127) << 23) : __uint_as_float(0x7fc00000u);
+          sl2 *= __uint_as_float((uint32_t)(e2 - 7 + 127) << 23);
           if (!TOKEN) sl2 *= __ldg(g.k_scale + sg.head);
           if (sl2 == 0.f) sl2 = 1.2e-38f;  // (0 * -inf of a masked key would be NaN)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (!PAIR && (i >> 3) != w) continue;
-            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t f[4];
+          for (int i = 0; i < 8; ++i) {  // 16 elements; of a shared tile the first warpgroup writes hi, the second lo
+            const uint32_t u[8] = {v[2 * i].x, v[2 * i].y, v[2 * i].z, v[2 * i].w,
+                                   v[2 * i + 1].x, v[2 * i + 1].y, v[2 * i + 1].z, v[2 * i + 1].w};
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              f[e] = pack2<true>(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
-            *reinterpret_cast<uint4*>(dst + (i >> 3) * kChunk + (((i ^ row) & 7) << 4)) =
-                make_uint4(f[0], f[1], f[2], f[3]);
+            for (int e = 0; e < 4; ++e) {
+              const float x0 = __uint_as_float(u[2 * e] << 16) * up, x1 = __uint_as_float(u[2 * e] & 0xffff0000u) * up;
+              const float x2 = __uint_as_float(u[2 * e + 1] << 16) * up;
+              const float x3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * up;
+              hi[e] = pack_codes(x0, x1) | (pack_codes(x2, x3) << 16);
+              const uint32_t h01 = widen_lo(hi[e]), h23 = widen_hi(hi[e]);
+              const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+              const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+              lo[e] = pack_codes(x0 - f01.x, x1 - f01.y) | (pack_codes(x2 - f23.x, x3 - f23.y) << 16);
+            }
+            uint8_t* at = dst + (((i ^ row) & 7) << 4);
+            if (PAIR || w == 0) *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (PAIR || w == 1) *reinterpret_cast<uint4*>(at + kChunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         fence_async();
@@ -525,7 +535,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       // divided, so that O stays an average of V rows whatever the rounding
       float ref = -INFINITY, l = 0.f, lu = 0.f;
       uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
-      for (int i = PAIR ? 0 : w; i < nt; i += PAIR ? 1 : 2) {
+      const int first = PAIR ? 0 : (w - tn) & 1;
+      for (int i = first; i < nt; i += C::AHEAD) {
         ok = mbar_wait<true>(s_full + w, (uint32_t)sn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
         if (!ok) break;
         ++sn;
@@ -582,8 +593,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
         }
         float inv_ref = 1.f;
         if constexpr (TOKEN) {
-          const int vi = base + item_v<PAIR>(i, nt);  // V's scales are there once it is converted
-          ok = mbar_wait<true>(full + vi % C::SLOTS, (uint32_t)(vi / C::SLOTS) & 1u, abort_flag, g.status,
+          const int ms = (tn + i) % C::M_SLOTS;  // V's scales are there once it is converted
+          ok = mbar_wait<true>(m_full + ms, (uint32_t)((tn + i) / C::M_SLOTS) & 1u, abort_flag, g.status,
                                FP_DEV_TIMEOUT);
           if (!ok) break;
           const int at = (tn + i) % kScales;
@@ -598,7 +609,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           inv_ref = __uint_as_float((v_exp == 254u ? 1u : 254u - max(v_exp, 27u)) << 23);
           if (v_exp == 254u) inv_ref *= 0.5f;
         }
-        if (i > (PAIR ? 0 : 1) && __any_sync(0xffffffffu, f != 1.f)) {
+        if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t r16[16];
@@ -702,7 +713,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           a.lse[(long long)(sg.head * a.G + h) * g.total_tokens + sg.off + tok] = lse2 * 0.69314718055994531f;
       };
       if (PAIR || nt == 1) {
-        if (PAIR || w == 0) {
+        if (PAIR || first == 0) {
           const float f = lu == 0.f ? 0.f : v_mul / lu;
 #pragma unroll 1
           for (int d0 = 0; d0 < D; d0 += 32) {
@@ -770,7 +781,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
         if (w == 0) store_lse(top, sum);
       }
       tc_fence_before();
-      base += 2 * nt;
       tn += nt;
     }
   }
