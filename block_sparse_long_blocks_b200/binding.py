@@ -8,6 +8,8 @@ The function names mirror the C ABI in ``include/flashprefill.h``.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from dataclasses import dataclass
@@ -17,6 +19,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libflashprefill.so")
+_CALLS_PATH = os.path.join(_PKG, "_calls.so")
 
 FP_BF16, FP_E4M3 = 0, 1
 STATUS = {0: "FP_OK", -1: "FP_ERR_INVALID_ARG", -2: "FP_ERR_UNSUPPORTED", -3: "FP_ERR_ALIGNMENT",
@@ -322,8 +325,26 @@ def fp_get_device_status(stream=None) -> int:
 # the paged cache and the decoding steps over it
 # ----------------------------------------------------------------------------
 
-# These calls run once per layer and step, on inputs of a few kilobytes, so what
-# they check per call is kept to comparisons (messages are built on failure).
+# The calls below run once per layer and decoding step, so their checks and the
+# call into the library are native (native/calls.cpp).
+
+_calls = None
+
+
+def _native():
+    """The module of the per-step calls, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        if not os.path.exists(_CALLS_PATH):
+            raise RuntimeError(f"{_CALLS_PATH} is missing: build it with `python -m block_sparse_long_blocks_b200.build`")
+        load()
+        loader = importlib.machinery.ExtensionFileLoader("_calls", _CALLS_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+        loader.exec_module(module)
+        module.bind(LIB_PATH)
+        _calls = module
+    return _calls
+
 
 def _refuse(fn: str, what: str):
     raise ValueError(f"{fn}: {what}")
@@ -331,22 +352,6 @@ def _refuse(fn: str, what: str):
 
 def _is_int32(t: torch.Tensor, dev: int, shape: tuple) -> bool:
     return t.dtype is torch.int32 and t.get_device() == dev and t.shape == shape and t.is_contiguous()
-
-
-def _is_rows(t: torch.Tensor, dev: int, shape: tuple) -> bool:
-    """bf16 [tokens, heads, d] whose tokens are contiguous, at any distance."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != shape:
-        return False
-    s = t.stride()
-    return s[2] == 1 and (s[1] == shape[2] or shape[1] == 1)
-
-
-def _launch_stream(fn: str, dev: int, stream) -> int:
-    """The stream of a call whose tensors live on device `dev`: launches go to the
-    current device, so the two have to agree."""
-    if torch.cuda.current_device() != dev:
-        _refuse(fn, f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 class Cache:
@@ -387,56 +392,31 @@ class Cache:
             page_size=page, num_pages=pages, max_pages_per_req=page_table.shape[1], k_pool=k_pool.data_ptr(),
             v_pool=v_pool.data_ptr(), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale), page_table=page_table.data_ptr(),
             kv_lens=kv_lens.data_ptr())
-        self.ref = ctypes.byref(self.p)
-
-
-def _rows(fn: str, cache: Cache, cu, k, v):
-    dev = cache.dev
-    if not _is_int32(cu, dev, (cache.batch + 1,)):
-        _refuse(fn, f"cu_tokens must be a contiguous int32 [{cache.batch + 1}] on cuda:{dev}")
-    total = k.shape[0]
-    shape = (total, cache.hkv, cache.head_dim)
-    if not (_is_rows(k, dev, shape) and _is_rows(v, dev, shape)):
-        _refuse(fn, f"k and v must be bfloat16 [tokens, {cache.hkv}, {cache.head_dim}] on cuda:{dev}, "
-                "contiguous within a token")
-    if total > 1:
-        return total, k.stride(0), v.stride(0)
-    row = cache.hkv * cache.head_dim  # (the stride of a single row is whatever its tensor happens to say)
-    return total, row, row
+        self.ref, self.addr = ctypes.byref(self.p), ctypes.addressof(self.p)
 
 
 def fp_cache_write(cache: Cache, cu_tokens, k, v, stream=None):
     """Writes new tokens' K and V (bf16 [tokens, hkv, d], any token stride) into the cache."""
-    total, ks, vs = _rows("fp_cache_write", cache, cu_tokens, k, v)
-    s = _launch_stream("fp_cache_write", cache.dev, stream)
-    code = load().fp_cache_write(cache.ref, cu_tokens.data_ptr(), total, k.data_ptr(), ks, v.data_ptr(), vs, s)
-    _check("fp_cache_write", code)
+    code = (_calls or _native()).cache_write(cache.addr, cache.dev, cu_tokens, k, v, stream)
+    if code:
+        _check("fp_cache_write", code)
 
 
 def fp_cache_read(cache: Cache, cu_tokens, k, v, starts=None, stream=None):
     """Reads cached tokens into k and v (bf16 [tokens, hkv, d]): the last ones of
     every request, or those from ``starts`` on."""
-    total, ks, vs = _rows("fp_cache_read", cache, cu_tokens, k, v)
-    if starts is not None and not _is_int32(starts, cache.dev, (cache.batch,)):
-        _refuse("fp_cache_read", f"starts must be a contiguous int32 [{cache.batch}] on cuda:{cache.dev}")
-    s = _launch_stream("fp_cache_read", cache.dev, stream)
-    code = load().fp_cache_read(cache.ref, cu_tokens.data_ptr(), total, _ptr(starts), k.data_ptr(), ks, v.data_ptr(),
-                                vs, s)
-    _check("fp_cache_read", code)
+    code = (_calls or _native()).cache_read(cache.addr, cache.dev, cu_tokens, k, v, starts, stream)
+    if code:
+        _check("fp_cache_read", code)
 
 
 def fp_cache_commit(cache: Cache, cu_tokens, total_tokens: int, accept, num_accept, new_lens, stream=None):
     """Moves the accepted new tokens' rows to the positions they keep and writes
     the requests' new lengths (``new_lens`` may be the cache's kv_lens)."""
-    fn, dev, R = "fp_cache_commit", cache.dev, cache.batch
-    if not (_is_int32(cu_tokens, dev, (R + 1,)) and _is_int32(num_accept, dev, (R,)) and _is_int32(new_lens, dev, (R,))
-            and accept.dim() == 2 and _is_int32(accept, dev, (R, accept.shape[1]))):
-        _refuse(fn, f"cu_tokens [{R + 1}], accept [{R}, max_accept], num_accept [{R}] and new_lens [{R}] must be "
-                f"contiguous int32 on cuda:{dev}")
-    s = _launch_stream(fn, dev, stream)
-    code = load().fp_cache_commit(cache.ref, cu_tokens.data_ptr(), total_tokens, accept.data_ptr(),
-                                  num_accept.data_ptr(), accept.shape[1], new_lens.data_ptr(), s)
-    _check(fn, code)
+    code = (_calls or _native()).cache_commit(cache.addr, cache.dev, cu_tokens, total_tokens, accept, num_accept,
+                                              new_lens, stream)
+    if code:
+        _check("fp_cache_commit", code)
 
 
 class Tree:
@@ -446,10 +426,8 @@ class Tree:
 
     def __init__(self, cache: Cache, hq: int, total_tokens: int, max_tokens: int, softmax_scale: float = 0.0):
         self.cache = cache
-        self.hq, self.total_tokens = hq, total_tokens
-        self.shape, self.lse_shape = (total_tokens, hq, cache.head_dim), (hq, total_tokens)
         self.p = TreeParams(hq=hq, total_tokens=total_tokens, max_tokens=max_tokens, softmax_scale=softmax_scale)
-        self.ref = ctypes.byref(self.p)
+        self.ref, self.addr = ctypes.byref(self.p), ctypes.addressof(self.p)
         if cache.dev < 0:
             _refuse("Tree", "the cache must be on a CUDA device")
         with torch.cuda.device(cache.dev):
@@ -465,31 +443,11 @@ def fp_tree_attention(plan: Tree, cu_tokens, q, o, mask=None, lse=None, stream=N
     over the cache into o (bf16, contiguous) and lse (float32 [hq, tokens]).
     mask: int32 [tokens, words], bit j: the row sees new token j of its request;
     without it a row sees the new tokens up to its own."""
-    fn, cache, p = "fp_tree_attention", plan.cache, plan.p
-    dev, shape = cache.dev, plan.shape
-    if not _is_int32(cu_tokens, dev, (cache.batch + 1,)):
-        _refuse(fn, f"cu_tokens must be a contiguous int32 [{cache.batch + 1}] on cuda:{dev}")
-    if not _is_rows(q, dev, shape):
-        _refuse(fn, f"q must be bfloat16 {shape} on cuda:{dev}, contiguous within a token")
-    if not (o.dtype is torch.bfloat16 and o.get_device() == dev and o.shape == shape and o.is_contiguous()):
-        _refuse(fn, f"o must be contiguous bfloat16 {shape} on cuda:{dev}")
-    lse_ptr = mask_ptr = None
-    words = 0
-    if lse is not None:
-        if not (lse.dtype is torch.float32 and lse.get_device() == dev and lse.shape == plan.lse_shape
-                and lse.is_contiguous()):
-            _refuse(fn, f"lse must be contiguous float32 {plan.lse_shape} on cuda:{dev}")
-        lse_ptr = lse.data_ptr()
-    if mask is not None:
-        if mask.dim() != 2 or not _is_int32(mask, dev, (shape[0], mask.shape[1])):
-            _refuse(fn, f"mask must be contiguous int32 [{shape[0]}, words] on cuda:{dev}")
-        mask_ptr, words = mask.data_ptr(), mask.shape[1]
-    s = _launch_stream(fn, dev, stream)
-    p.cu_tokens, p.mask, p.mask_words = cu_tokens.data_ptr(), mask_ptr, words
-    p.q_stride = q.stride(0) if shape[0] > 1 else 0
-    code = load().fp_tree_attention(cache.ref, plan.ref, q.data_ptr(), o.data_ptr(), lse_ptr, plan.ws_ptr,
-                                    plan.ws_bytes, s)
-    _check(fn, code)
+    cache = plan.cache
+    code = (_calls or _native()).tree_attention(cache.addr, cache.dev, plan.addr, plan.ws_ptr, plan.ws_bytes, cu_tokens,
+                                                q, o, mask, lse, stream)
+    if code:
+        _check("fp_tree_attention", code)
 
 
 def run_path(p: Params, q, k, v, bufs: Buffers, paged: bool = False, fused: bool = True, stream=None):

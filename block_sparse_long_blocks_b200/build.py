@@ -6,6 +6,9 @@ Compiles each ``csrc/*.cu`` to an object (in parallel) and links one shared
 library with the CUDA runtime linked statically, so the library depends only on
 the driver. The build is skipped when the library is newer than every source.
 
+``build_calls()`` compiles ``native/calls.cpp``, the per-step calls' CPython module,
+against the installed torch into ``_calls.so``.
+
 ``build_variant(name, defines)`` builds the same sources with extra
 preprocessor definitions into ``libflashprefill_<name>.so`` (objects in
 ``_build_<name>/``); the tests use one with a microsecond pipeline-wait limit
@@ -20,6 +23,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -101,12 +105,38 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False,
     return lib
 
 
+CALLS_SRC = os.path.join(PKG, "native", "calls.cpp")
+CALLS = os.path.join(PKG, "_calls.so")
+
+
+def build_calls(force: bool = False) -> str:
+    """The CPython module of the per-step calls (host code only)."""
+    newest = max(os.path.getmtime(p) for p in (CALLS_SRC, os.path.join(INCLUDE, "flashprefill.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return CALLS
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    dirs = [sysconfig.get_paths()["include"], f"{root}/include", f"{root}/include/torch/csrc/api/include",
+            f"{cuda}/include", INCLUDE]
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", CALLS_SRC,
+           "-o", tmp, *[f"-I{d}" for d in dirs], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
     ap.add_argument("--verbose-ptxas", action="store_true")
     a = ap.parse_args()
     print(build(force=a.force, verbose_ptxas=a.verbose_ptxas))
+    print(build_calls(force=a.force))
 
 
 if __name__ == "__main__":

@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < NB; ++b) neg[b] = ref[b] == -INFINITY ? 0.f : (E4M3 ? kShift - ref[b] : -ref[b]);
 
       if (ok) ok = mbar_wait<true>(vfull, vphase, abort_flag, g.status, FP_DEV_TIMEOUT);
-      float inv_ref = 1.f;
+      [[maybe_unused]] float inv_ref = 1.f;
       if constexpr (TOKEN) {
         // the largest v_scale of these keys (scales are not negative: they compare as integers)
         uint32_t top = 0;
@@ -832,9 +832,12 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
 // host side
 // ---------------------------------------------------------------------------
 int sm_count() {
+  static std::atomic<int> counts[64];  // per device, 0: not asked yet
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < 64) counts[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -846,7 +849,8 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
   using C = Cfg<E4M3, D, NB>;
   auto kern = tree_kernel<E4M3, TOKEN, D, NB>;
   const int smem = C::SMEM_FIXED + (a.g.R + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_shared(kern, allowed);
   if (e != cudaSuccess) return e;
   kern<<<a.grid, kThreads, smem, s>>>(mk, mv, a);
   return cudaGetLastError();

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "internal.cuh"
 #include "sm100.cuh"
 
@@ -224,6 +226,20 @@ __device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg
     if (!isfinite(v[2])) acc.z += v[2];
     if (!isfinite(v[3])) acc.w += v[3];
   }
+}
+
+// Lets a kernel take all the dynamic shared memory a CTA can have: once per kernel and
+// device, as the runtime call costs a fifth of a launch.
+template <class K>
+cudaError_t allow_shared(K kern, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // The kernel for many rows (tree_wide.cu): a.rows is 128 or 256.

@@ -798,7 +798,8 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
   // more than half of the SM's shared memory: one CTA per SM, so that the
   // 512-column TMEM allocation never waits for a co-resident CTA
   const int want = C::SMEM_FIXED + (a.g.R + 1) * 4, smem = want > 120 * 1024 ? want : 120 * 1024;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_shared(kern, allowed);
   if (e != cudaSuccess) return e;
   kern<<<a.grid, Roles<E4M3>::THREADS, smem, s>>>(mk, mv, a);
   return cudaGetLastError();
