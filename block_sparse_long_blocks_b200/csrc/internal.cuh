@@ -135,9 +135,11 @@ struct CacheGeometry {
 
 // Rows, new tokens and cached length of request r; false (n = 0) when the
 // request's arrays do not fit, with FP_DEV_BAD_SEQLENS set.
+// READ_ONLY: the kernel does not write kv_lens (fp_cache_commit may).
+template <bool READ_ONLY = false>
 __device__ __forceinline__ bool cache_span(const CacheGeometry& g, int r, int& off, int& n, int& kv) {
   const int a = __ldg(g.cu + r), b = __ldg(g.cu + r + 1);
-  kv = __ldcg(g.kv_lens + r);  // (not the read-only path: fp_cache_commit may write it)
+  kv = READ_ONLY ? __ldg(g.kv_lens + r) : __ldcg(g.kv_lens + r);
   off = a;
   n = b - a;
   if (a < 0 || n < 0 || b > g.total_tokens || n > kv || kv > (long long)g.max_pages * g.page_size) {

@@ -131,7 +131,7 @@ struct Cfg {
   static_assert(QT * 16 * D * ES <= RED, "Q lies in the same place while the keys are read");
   static constexpr int SMEM_FIXED = 1024 + SLOTS * SLOT + RED + (2 * kWarps + 1) * ROWS * 4 + 2 * SLOTS * 8 + 64;
   static_assert(D * ES % 128 == 0, "head dim 128, or 64 with bf16");
-  static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
+  static_assert(SMEM_FIXED + kAxisBytesMax <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = misc;
   int* warp_sum = misc + 1;                     // [12]
   volatile int* s_odd = misc + 13;              // [2], by segment parity: see below
-  int* pre = misc + 16;                         // [R + 1]
+  Axis axis(misc + 16, a.g.R);
 
   const CacheGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_odd[0] = s_odd[1] = 0;
     fence_barrier_init();
   }
-  prefix_tiles(a, pre, warp_sum);  // (its barriers publish the initialisation above)
-  const int total = pre[g.R];
+  axis.build(a, warp_sum);  // (its barrier publishes the initialisation above)
+  const int total = axis.total();
   const int share = share_of(total, a.grid);
   const long long x_first = (long long)blockIdx.x * share;
   if (x_first >= total) return;
@@ -195,9 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int slot = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
-    int r = request_of(pre, g.R, x_begin);
+    int r = axis.request_of(x_begin);
     for (int x = x_begin; x < x_end && ok;) {
-      const Segment sg = segment_at(a, pre, x, x_end, r);
+      const Segment sg = segment_at(a, axis, x, x_end, r);
       const int32_t* row = g.table + (long long)sg.r * g.max_pages;
       auto page_at = [&](int tile) {  // the page of this lane's part of a tile
         const int tok = tile * C::TILE + lane * sub_rows;
@@ -294,10 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
-  int r = request_of(pre, g.R, x_begin);
+  int r = axis.request_of(x_begin);
   int segment = 0;
   for (int x = x_begin; x < x_end; ++segment) {
-    const Segment sg = segment_at(a, pre, x, x_end, r);
+    const Segment sg = segment_at(a, axis, x, x_end, r);
     x += sg.t1 - sg.t0;
     const int nrows = sg.n * a.G;
     // ---- Q to shared memory, as the rows of A tiles
@@ -754,76 +754,96 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // combining partial rows
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
 
 // One CTA per (token, query head) row: the partial rows its unit left in the
-// workspace, in CTA order; its four warps take every fourth one.
+// workspace, in CTA order. Every warp holds all their weights (at most one
+// partial row per SM: a few registers a lane) and sums every eighth row, with
+// up to four loads in flight; a loop of dependent loads, weight before row, took 8-16 us.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
-  extern __shared__ int pre[];  // [R + 1]
-  __shared__ int warp_sum[kMergeThreads / 32];
-  __shared__ float acc[kMergeThreads / 32][D];
+  constexpr int WARPS = kMergeThreads / 32;
+  constexpr int MOST = 8;       // partial rows per lane: up to 256 SMs
   constexpr int PER = D / 32;   // columns per lane
+  extern __shared__ int4 axis_mem[];
+  __shared__ int warp_sum[WARPS];
+  __shared__ float acc[WARPS][D];
   const CacheGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int token = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
-  prefix_tiles(a, pre, warp_sum);
-  const int total = pre[g.R];
+  const int token = blockIdx.x / a.Hq, hq = blockIdx.x - token * a.Hq;
+  Axis axis(axis_mem, g.R);
+  axis.build(a, warp_sum);
+  const int total = axis.total();
   // the request of this token
-  int lo = 0, hi = g.R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
+  int r = 0;
+  for (int hi = g.R - 1; r < hi;) {
+    const int mid = (r + hi) >> 1;
     if (__ldg(g.cu + mid + 1) > token) hi = mid;
-    else lo = mid + 1;
+    else r = mid + 1;
   }
-  int off, n, kv, nt, nm;
-  request_tiles(a, lo, off, n, kv, nt, nm);
+  const Span sp = axis.span(a, r);
   // every thread waits, also those with nothing to do: this grid is not to end
   // before the one that it depends on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (nt == 0 || token < off || token >= off + n) return;
-  const int row = (token - off) * a.G + hq % a.G, head = hq / a.G;
-  const int x0 = pre[lo] + (head * nm + row / a.rows) * nt, x1 = x0 + nt;
+  if (sp.n == 0 || token < sp.off || token >= sp.off + sp.n) return;
+  const int nt = tiles_of(a, sp), head = hq / a.G, row = (token - sp.off) * a.G + hq - head * a.G;
+  const int x0 = axis.first(r) + (head * units_of(a, sp) + (row >> a.rows_shift)) * nt, x1 = x0 + nt;
   const int share = share_of(total, a.grid);
   const int c0 = x0 / share, c1 = (x1 - 1) / share;
   if (c0 == c1) return;  // one CTA had the whole unit and finished it
-  const int lr = row % a.rows;
+  const int lr = row & (a.rows - 1);
   // its partial in CTA c: the CTA's first segment, unless the unit begins inside the CTA's share
   auto part = [&](int c) { return (long long)(2 * c + ((long long)c * share < x0 ? 1 : 0)) * a.rows + lr; };
-  float big = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) big = fmaxf(big, __ldcg(a.part_lse + part(c)));
+  float w[MOST], big = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    const int c = c0 + lane + 32 * k;
+    w[k] = c <= c1 ? __ldcg(a.part_lse + part(c)) : -INFINITY;
+    big = fmaxf(big, w[k]);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
   const float ref = big == -INFINITY ? 0.f : big;
   float sum = 0.f, v[PER];
 #pragma unroll
-  for (int e = 0; e < PER; ++e) v[e] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += kMergeThreads / 32) {
-    const long long p = part(c);
-    const float w = exp2_fast(__ldcg(a.part_lse + p) - ref);
-    const float* src = a.part_o + p * D + lane * PER;
-    float y[PER];
-    if constexpr (PER == 4) {
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-      y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
-    } else {
-      const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-      y[0] = f.x, y[1] = f.y;
-    }
-    sum += w;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) v[e] += w == 0.f ? 0.f : w * y[e];
+  for (int k = 0; k < MOST; ++k) {
+    w[k] = exp2_fast(w[k] - ref);
+    sum += w[k];
   }
-  __shared__ float sums[kMergeThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+  for (int e = 0; e < PER; ++e) v[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    if (c0 + 32 * k > c1) break;
+#pragma unroll
+    for (int j = 0; j < 32 / WARPS; ++j) {  // (loads of one round are independent)
+      const int l = warp + j * WARPS, c = c0 + 32 * k + l;
+      const float f = __shfl_sync(0xffffffffu, w[k], l);
+      if (c > c1) continue;
+      const float* src = a.part_o + part(c) * D + lane * PER;
+      float y[PER];
+      if constexpr (PER == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+        y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        y[0] = x.x, y[1] = x.y;
+      }
+#pragma unroll
+      for (int e = 0; e < PER; ++e) v[e] += f == 0.f ? 0.f : f * y[e];
+    }
+  }
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[warp][lane * PER + e] = v[e];
-  if (lane == 0) sums[warp] = sum;
   __syncthreads();
-  sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int d = threadIdx.x; d < D; d += kMergeThreads)
-    a.o[((long long)token * a.Hq + hq) * D + d] =
-        __float2bfloat16_rn(((acc[0][d] + acc[1][d]) + (acc[2][d] + acc[3][d])) * inv);
+  if (threadIdx.x < D) {
+    float o = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) o += acc[k][threadIdx.x];
+    a.o[((long long)token * a.Hq + hq) * D + threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+  }
   if (a.lse && threadIdx.x == 0)
     a.lse[(long long)hq * g.total_tokens + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
@@ -837,6 +857,7 @@ int sm_count() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
   if (dev < 64 && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  n = n < 256 ? n : 256;
   if (dev < 64) counts[dev].store(n, std::memory_order_relaxed);
   return n;
 }
@@ -844,11 +865,17 @@ int sm_count() {
 // Rows per unit: the kernel here holds 8 or 16, the one for many rows (tree_wide.cu) one or two M-tiles of 128.
 int unit_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 128 ? 128 : 256; }
 
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
 template <bool E4M3, bool TOKEN, int D, int NB>
 cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   using C = Cfg<E4M3, D, NB>;
   auto kern = tree_kernel<E4M3, TOKEN, D, NB>;
-  const int smem = C::SMEM_FIXED + (a.g.R + 1) * 4;
+  const int smem = C::SMEM_FIXED + axis_bytes(a.g.R);
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_shared(kern, allowed);
   if (e != cudaSuccess) return e;
@@ -861,7 +888,7 @@ cudaError_t run_merge(const TreeArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.g.total_tokens * a.Hq));
   cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = (size_t)(a.g.R + 1) * 4;
+  cfg.dynamicSmemBytes = (size_t)axis_bytes(a.g.R);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -902,8 +929,10 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   a.lse = lse;
   const double scale = t.softmax_scale > 0.f ? (double)t.softmax_scale : 1.0 / std::sqrt((double)g.d);
   a.scale_log2 = (float)(scale * 1.4426950408889634);
-  a.grid = sm_count();
+  a.grid = sm_count();  // (at most 256: the combining kernel's registers)
   a.tile = a.rows <= 16 ? kTileBytes / (g.d * (g.e4m3 ? 1 : 2)) : 128;
+  a.rows_shift = log2_of(a.rows);
+  a.tile_shift = log2_of(a.tile);
   const size_t rows = (size_t)2 * a.grid * a.rows;
   a.part_o = static_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pad256(rows * g.d * sizeof(float)));

@@ -24,8 +24,8 @@ struct TreeArgs {
   CacheGeometry g;
   int Hq, G;
   int max_tokens;
-  int rows;               // rows per M-tile unit
-  int tile;               // keys per tile
+  int rows, rows_shift;   // rows per unit, a power of two
+  int tile, tile_shift;   // keys per tile, a power of two
   const uint32_t* mask;
   int mask_words;
   const __nv_bfloat16* q;
@@ -41,64 +41,108 @@ struct TreeArgs {
 // ---------------------------------------------------------------------------
 // the axis of tiles
 // ---------------------------------------------------------------------------
-// Tiles of the keys of request r, and M-tile units per KV head (0 for a request
-// that is empty, or rejected).
-__device__ __forceinline__ void request_tiles(const TreeArgs& a, int r, int& off, int& n, int& kv, int& nt, int& nm) {
-  nt = nm = 0;
-  if (!cache_span(a.g, r, off, n, kv)) return;
-  if (n > a.max_tokens) {
+// Where a request's rows and keys lie (n = 0: empty, or rejected).
+struct Span {
+  int off, n, kv;
+};
+
+__device__ __forceinline__ Span load_span(const TreeArgs& a, int r) {
+  Span s;
+  if (!cache_span<true>(a.g, r, s.off, s.n, s.kv)) {
+    s.n = 0;
+  } else if (s.n > a.max_tokens) {
     atomicOr(a.g.status, FP_DEV_BAD_SEQLENS);
-    n = 0;
+    s.n = 0;
   }
-  if (n == 0) return;
-  nt = (kv + a.tile - 1) / a.tile;
-  nm = (n * a.G + a.rows - 1) / a.rows;
+  return s;
 }
 
-// Exclusive prefix of the requests' tile counts into pre[0 .. R] (all threads of
-// the block; `warp_sum` has one int per warp). The host bounds the total by INT_MAX.
-__device__ __forceinline__ void prefix_tiles(const TreeArgs& a, int* pre, int* warp_sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int carry = 0;
-  for (int r0 = 0; r0 < a.g.R; r0 += blockDim.x) {
-    const int r = r0 + threadIdx.x;
-    int mine = 0;
-    if (r < a.g.R) {
-      int off, n, kv, nt, nm;
-      request_tiles(a, r, off, n, kv, nt, nm);
-      mine = nt * nm * a.g.Hkv;
-    }
-    int incl = mine;
+// Tiles of a request's keys, and units per KV head.
+__device__ __forceinline__ int tiles_of(const TreeArgs& a, const Span& s) {
+  return s.n == 0 ? 0 : (s.kv + a.tile - 1) >> a.tile_shift;
+}
+__device__ __forceinline__ int units_of(const TreeArgs& a, const Span& s) {
+  return (s.n * a.G + a.rows - 1) >> a.rows_shift;
+}
+
+// Requests whose spans are kept in shared memory beside the prefix (16 bytes each; of more, 4 bytes each). Every
+// role of every CTA asks for them at each segment: loads of the same few lines by all of the GPU's warps took
+// 2700 clocks where shared memory takes 100.
+constexpr int kSpanTable = 1024;
+__host__ __device__ constexpr int axis_bytes(int R) { return (R + 1) * (R <= kSpanTable ? 16 : 4); }
+constexpr int kAxisBytesMax = axis_bytes(kSpanTable) > axis_bytes(4096) ? axis_bytes(kSpanTable) : axis_bytes(4096);
+
+// The requests along the axis: first tile of each, and its span.
+struct Axis {
+  int* mem;  // axis_bytes(R) of shared memory, 16-byte aligned
+  int R;
+  bool spans;
+
+  __device__ __forceinline__ Axis(void* m, int requests)
+      : mem(static_cast<int*>(m)), R(requests), spans(requests <= kSpanTable) {}
+  __device__ __forceinline__ int first(int r) const { return spans ? mem[4 * r] : mem[r]; }
+  __device__ __forceinline__ int total() const { return first(R); }
+  __device__ __forceinline__ Span span(const TreeArgs& a, int r) const {
+    if (!spans) return load_span(a, r);
+    const int4 v = reinterpret_cast<const int4*>(mem)[r];
+    return {v.y, v.z, v.w};
+  }
+  __device__ __forceinline__ void put(int r, int at, const Span& s) {
+    if (spans) reinterpret_cast<int4*>(mem)[r] = make_int4(at, s.off, s.n, s.kv);
+    else mem[r] = at;
+  }
+
+  // All threads of the block; `warp_sum` has one int per warp. Ends with a block barrier. The host bounds the
+  // total by INT_MAX.
+  __device__ __forceinline__ void build(const TreeArgs& a, int* warp_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int carry = 0;
+    const int threads = R <= 32 ? 32 : blockDim.x;  // few requests: one warp, without barriers
+    if (threadIdx.x < threads) {
+      for (int r0 = 0; r0 < R; r0 += threads) {
+        const int r = r0 + threadIdx.x;
+        Span s = {0, 0, 0};
+        int mine = 0;
+        if (r < R) {
+          s = load_span(a, r);
+          mine = tiles_of(a, s) * units_of(a, s) * a.g.Hkv;
+        }
+        int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        int before = carry;
+        if (threads == 32) {
+          carry += __shfl_sync(0xffffffffu, incl, 31);
+        } else {
+          if (lane == 31) warp_sum[warp] = incl;
+          __syncthreads();
+          for (int w = 0; w < warps; ++w) {
+            if (w < warp) before += warp_sum[w];
+            carry += warp_sum[w];
+          }
+          __syncthreads();
+        }
+        if (r < R) put(r, before + incl - mine, s);
+      }
+      if (threadIdx.x == 0) put(R, carry, {0, 0, 0});
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int before = carry, all = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) before += warp_sum[w];
-      all += warp_sum[w];
-    }
-    if (r < a.g.R) pre[r] = before + incl - mine;
-    carry += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) pre[a.g.R] = carry;
-  __syncthreads();
-}
 
-// The request whose tiles hold tile x (0 <= x < pre[R]).
-__device__ __forceinline__ int request_of(const int* pre, int R, int x) {
-  int lo = 0, hi = R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid + 1] > x) hi = mid;
-    else lo = mid + 1;
+  // The request whose tiles hold tile x (0 <= x < total).
+  __device__ __forceinline__ int request_of(int x) const {
+    int lo = 0, hi = R - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (first(mid + 1) > x) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
   }
-  return lo;
-}
+};
 
 __device__ __forceinline__ int share_of(int total, int grid) { return (total + grid - 1) / grid; }
 
@@ -110,18 +154,20 @@ struct Segment {
   __device__ __forceinline__ bool whole() const { return t1 - t0 == nt; }
 };
 
-__device__ __forceinline__ Segment segment_at(const TreeArgs& a, const int* pre, int x, int end, int& r) {
-  while (pre[r + 1] <= x) ++r;
+__device__ __forceinline__ Segment segment_at(const TreeArgs& a, const Axis& axis, int x, int end, int& r) {
+  while (axis.first(r + 1) <= x) ++r;
+  const Span sp = axis.span(a, r);
   Segment s;
-  int nm;
   s.r = r;
-  request_tiles(a, r, s.off, s.n, s.kv, s.nt, nm);
+  s.off = sp.off;
+  s.n = sp.n;
+  s.kv = sp.kv;
+  s.nt = tiles_of(a, sp);
   s.base = s.kv - s.n;
-  const int y = x - pre[r];
-  const int unit = y / s.nt;
+  const int nm = units_of(a, sp), y = x - axis.first(r), unit = y / s.nt;
   s.t0 = y - unit * s.nt;
   s.t1 = min(s.nt, s.t0 + (end - x));
-  s.head = unit / nm;
+  s.head = nm == 1 ? unit : unit / nm;
   s.row0 = (unit - s.head * nm) * a.rows;
   return s;
 }

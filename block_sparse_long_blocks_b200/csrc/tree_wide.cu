@@ -82,7 +82,7 @@ struct Cfg {
   static constexpr int SMEM_FIXED = 1024 + Q + (K_SLOTS + V_SLOTS) * LOAD + W_SLOTS * TILE +
                                     (E4M3 ? kScales * 2 * kKeys * 4 : 0) + 128 * 16 + NUM_BARS * 8 + 336;
   static constexpr int COLS = Q / 512 < D ? Q / 512 : D;  // columns of O per round in which two warpgroups' O meet
-  static_assert(SMEM_FIXED + 4097 * 4 <= 227 * 1024, "shared memory");
+  static_assert(SMEM_FIXED + kAxisBytesMax <= 227 * 1024, "shared memory");
   static_assert(K_SLOTS % 2 == 0, "a slot is of one issuer");
   static_assert(COLS % 32 == 0 && D % COLS == 0, "rounds of whole TMEM loads");
 };
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   int* warp_sum = reinterpret_cast<int*>(tmem_slot + 2);             // [16]
   volatile uint32_t* s_vmax = tmem_slot + 18;                        // [kScales][4]
   volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 50);  // [kFlags][4]
-  int* pre = reinterpret_cast<int*>(tmem_slot + 82);                 // [R + 1]
+  Axis axis(tmem_slot + 84, a.g.R);
 
   const CacheGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -179,24 +179,26 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  prefix_tiles(a, pre, warp_sum);  // (its barriers publish the initialisation above)
-  const int total = pre[g.R];
-  const int share = share_of(total, a.grid);
-  const long long x_first = (long long)blockIdx.x * share;
-  if (x_first >= total) return;
-  const int x_begin = (int)x_first, x_end = min(total, x_begin + share);
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  axis.build(a, warp_sum);  // (its barrier publishes the initialisation above)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int total = axis.total();
+  const int share = share_of(total, a.grid);
+  const long long x_first = (long long)blockIdx.x * share;
+  if (x_first >= total) {
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int x_begin = (int)x_first, x_end = min(total, x_begin + share);
   if (warp >= 8) reg_dealloc<L::CONTROL_REGS>();
 
   bool ok = true;
-  int r = request_of(pre, g.R, x_begin);
+  int r = axis.request_of(x_begin);
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
     if (lane == 0) {
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     const int sub_rows = min(g.page_size, kKeys), sub_max = kKeys / sub_rows;  // sub_max <= 8
     int kn = 0, vn = 0;  // K and V tiles issued
     for (int x = x_begin; x < x_end && ok;) {
-      const Segment sg = segment_at(a, pre, x, x_end, r);
+      const Segment sg = segment_at(a, axis, x, x_end, r);
       const int nt = sg.t1 - sg.t0;
       x += nt;
       const int32_t* row = g.table + (long long)sg.r * g.max_pages;
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       int tn = 0, qn = 0, pn = 0, turns = 0;
       if (PAIR && w == 1) mbar_arrive(turn);  // the first turn is issuer 0's
       for (int x = x_begin; x < x_end && ok;) {
-        const Segment sg = segment_at(a, pre, x, x_end, r);
+        const Segment sg = segment_at(a, axis, x, x_end, r);
         const int nt = sg.t1 - sg.t0;
         x += nt;
         const int first = PAIR ? 0 : (w - tn) & 1;  // tiles first, first + AHEAD, ...
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     const int ct = threadIdx.x - L::CONVERT_WARP * 32, cw = warp - L::CONVERT_WARP;
     int tn = 0, segment = 0;
     for (int x = x_begin; x < x_end && ok; ++segment) {
-      const Segment sg = segment_at(a, pre, x, x_end, r);
+      const Segment sg = segment_at(a, axis, x, x_end, r);
       const int nt = sg.t1 - sg.t0;
       x += nt;
       bool fresh = true;  // the segment's flag is not cleared yet
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     const uint32_t tO = tmem + lane_base + 256 + w * 128;
     int tn = 0, sn = 0, on = 0, hn = 0, segment = 0;
     for (int x = x_begin; x < x_end; ++segment) {
-      const Segment sg = segment_at(a, pre, x, x_end, r);
+      const Segment sg = segment_at(a, axis, x, x_end, r);
       const int nt = sg.t1 - sg.t0;
       x += nt;
       const int lr = PAIR ? w * 128 + row : row, rho = sg.row0 + lr;
@@ -797,7 +799,7 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
   auto kern = wide_kernel<E4M3, TOKEN, D, PAIR>;
   // more than half of the SM's shared memory: one CTA per SM, so that the
   // 512-column TMEM allocation never waits for a co-resident CTA
-  const int want = C::SMEM_FIXED + (a.g.R + 1) * 4, smem = want > 120 * 1024 ? want : 120 * 1024;
+  const int want = C::SMEM_FIXED + axis_bytes(a.g.R), smem = want > 120 * 1024 ? want : 120 * 1024;
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_shared(kern, allowed);
   if (e != cudaSuccess) return e;
