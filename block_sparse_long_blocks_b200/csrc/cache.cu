@@ -1,28 +1,32 @@
 // The paged cache's own kernels: tokens into it (quantised on the way), tokens
 // out of it, and the accepted drafted tokens to their final slots.
 //
-// Write and read move every element once and compute next to nothing, so HBM
-// bounds them: a cached row is hkv * d contiguous elements, so 16-byte vectors
-// along it coalesce whatever the head count, and each thread keeps several
-// vectors of K and of V in flight. The chain cu_tokens -> kv_lens -> page table
-// that leads to a row's slot is walked once per CTA (by one warp, for all of the
-// CTA's tokens) while the first vectors are already on their way.
+// Write and read move every element once and compute little, so HBM bounds them:
+// a cached row is hkv * d contiguous elements, so vectors of eight of them (16
+// bytes of bf16, 8 of e4m3) along it coalesce whatever the head count, in the
+// loads and in the stores, and each thread keeps several vectors of K and of V
+// in flight. The chain cu_tokens -> kv_lens -> page table that leads to a row's
+// slot is walked once per CTA (by one warp, for all of the CTA's tokens) while
+// the first vectors are already on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "internal.cuh"
+#include "packed.cuh"
 
 namespace fp {
 
+using namespace packed;
+
 namespace {
 
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256, kMoveCtas = 5;  // CTAs per SM (48 registers a thread)
 constexpr int kMaxTokensPerCta = 64;
 enum Format { kBf16 = 0, kHeadScale = 1, kTokenScale = 2 };
 
-// Elements per thread and step: one 16-byte vector of the cached row.
-template <int FMT>
-constexpr int kVec = FMT == kBf16 ? 8 : 16;
+constexpr int kVec = 8;  // elements per thread and step
 
 // The request that row t belongs to: the first r with cu[r + 1] > t (the last
 // request if there is none; the caller checks the span). All lanes of the warp
@@ -113,33 +117,60 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
   return h;
 }
 
-// 16 bf16 elements as loaded (two vectors) -> 16 codes of x / scale.
-__device__ __forceinline__ uint4 quantise16(const uint4 (&in)[2], float scale) {
-  const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b, c, d;
-    unpack_bf16(w[2 * i], a, b);
-    unpack_bf16(w[2 * i + 1], c, d);
-    out[i] = pack_e4m3(__fdiv_rn(a, scale), __fdiv_rn(b, scale)) |
-             (pack_e4m3(__fdiv_rn(c, scale), __fdiv_rn(d, scale)) << 16);
-  }
-  return make_uint4(out[0], out[1], out[2], out[3]);
+// What x is divided by, as quantise() takes it.
+struct Divisor {
+  float scale, inv;
+  bool plain;  // neither the reciprocal nor a product of it leaves the normal range where it matters
+};
+__device__ __forceinline__ Divisor divisor(float scale) {
+  const float s = scale == 0.f ? 1.f : scale;
+  return {s, __frcp_rn(s), s >= 0x1p-80f && s <= 0x1p80f};
 }
 
-// max |x| over the eight lanes that hold one head's 128 elements (NaN does not count)
-__device__ __forceinline__ float head_absmax(const uint4 (&in)[2]) {
-  const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
+// Eight bf16 elements -> eight codes of x / scale, IEEE division. With y the
+// correctly rounded reciprocal of s, q = x y and r = x - q s (exact in a fused
+// multiply-add), q + r y is the correctly rounded quotient (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990): three packed instructions for two elements. The general division took
+// about twelve each and set the pace (4.2 of the 6.5 TB/s).
+__device__ __forceinline__ uint2 quantise(const uint4& in, const Divisor& d) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  uint32_t code[4];
+  const uint64_t y = f2_pack(d.inv, d.inv), ns = f2_pack(-d.scale, -d.scale);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack_bf16(w[i], a, b);
+    float qa, qb;
+    if (d.plain) {
+      const uint64_t x = f2_pack(a, b), q = f2_mul(x, y);
+      float pa, pb;
+      f2_unpack(q, pa, pb);
+      f2_unpack(f2_fma(f2_fma(q, ns, x), y, q), qa, qb);
+      // (far beyond the largest code the estimate does, and the correction may overflow)
+      qa = fabsf(pa) < 1024.f ? qa : pa;
+      qb = fabsf(pb) < 1024.f ? qb : pb;
+    } else {
+      qa = __fdiv_rn(a, d.scale);
+      qb = __fdiv_rn(b, d.scale);
+    }
+    code[i] = pack_e4m3(qa, qb);
+  }
+  return make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+}
+
+// max |x| over the sixteen lanes that hold one head's 128 elements (NaN does not count)
+__device__ __forceinline__ float head_absmax(const uint4& in) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     float a, b;
     unpack_bf16(w[i], a, b);
     m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
   }
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o, 8));
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o, 16));
   return m;
 }
 
@@ -151,6 +182,7 @@ struct MoveArgs {
   long long k_stride, v_stride;  // bytes between tokens
   int tokens;                    // per CTA
   int vecs;                      // vectors per cached row of K (and of V)
+  uint32_t vecs_inv;             // ceil(2^32 / vecs): i / vecs = (i * vecs_inv) >> 32 below 2^32 / vecs
 };
 
 // Cached row -> (page, slot-in-page) parts of the token scale's address.
@@ -160,64 +192,55 @@ __device__ __forceinline__ long long scale_index(const CacheGeometry& g, long lo
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kMoveThreads) cache_write_kernel(const MoveArgs a) {
-  constexpr int V = kVec<FMT>, L = V / 8;  // elements, and 16-byte loads, per vector
-  constexpr int U = 2;                     // vectors of K and of V in flight per thread
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_write_kernel(const MoveArgs a) {
+  constexpr int U = 2;  // vectors of K and of V in flight per thread
   __shared__ long long slot[kMaxTokensPerCta];
   const CacheGeometry& g = a.g;
   const int t0 = blockIdx.x * a.tokens;
   const int nt = min(a.tokens, g.total_tokens - t0);
   const int items = nt * a.vecs;
-  // rounded up to whole warps: the absmax shuffles need their eight lanes
   const int rounds = (items + U * kMoveThreads - 1) / (U * kMoveThreads);
-  uint4 in[2][U][L];
-  auto load = [&](int round) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = (round * U + u) * kMoveThreads + threadIdx.x;
-      if (i < items) {
-        const int t = i / a.vecs, x = i - t * a.vecs;
-        const uint8_t* kp = a.k + (t0 + t) * a.k_stride + (long long)x * (V * 2);
-        const uint8_t* vp = a.v + (t0 + t) * a.v_stride + (long long)x * (V * 2);
-#pragma unroll
-        for (int l = 0; l < L; ++l) {
-          in[0][u][l] = load_stream(kp + l * 16);
-          in[1][u][l] = load_stream(vp + l * 16);
-        }
-      }
+  uint4 in[2][U];
+  auto load = [&](int round, int u) {
+    const int i = (round * U + u) * kMoveThreads + threadIdx.x;
+    if (i < items) {
+      const int t = __umulhi(i, a.vecs_inv), x = i - t * a.vecs;
+      in[0][u] = load_stream(a.k + (t0 + t) * a.k_stride + x * 16);
+      in[1][u] = load_stream(a.v + (t0 + t) * a.v_stride + x * 16);
     }
   };
-  load(0);
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(0, u);
   find_slots(g, a.starts, t0, nt, slot);
   for (int round = 0; round < rounds; ++round) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = (round * U + u) * kMoveThreads + threadIdx.x;
+      // (whole warps go on: the absmax shuffles need their sixteen lanes)
       if (__all_sync(0xffffffffu, i >= items)) continue;
-      const int t = min(i, items - 1) / a.vecs, x = min(i, items - 1) - t * a.vecs;
+      const int j = min(i, items - 1), t = __umulhi(j, a.vecs_inv), x = j - t * a.vecs;
       const long long s = i < items ? slot[t] : kSkip;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         uint8_t* pool = which ? g.v_pool : g.k_pool;
-        float* scales = which ? g.v_scale : g.k_scale;
-        uint4 out;
         if constexpr (FMT == kBf16) {
-          out = in[which][u][0];
+          if (s >= 0) reinterpret_cast<uint4*>(pool)[s * a.vecs + x] = in[which][u];
         } else {
-          const int head = x / (128 / V);
+          float* scales = which ? g.v_scale : g.k_scale;
+          const int head = x >> 4;
           float sc;
           if constexpr (FMT == kTokenScale) {
             sc = __fdiv_rn(head_absmax(in[which][u]), 448.f);
-            if (s >= 0 && x % (128 / V) == 0) scales[scale_index(g, s, head)] = sc;
+            if (s >= 0 && (x & 15) == 0) scales[scale_index(g, s, head)] = sc;
           } else {
             sc = __ldg(scales + head);
           }
-          out = quantise16(in[which][u], sc == 0.f ? 1.f : sc);
+          const uint2 codes = quantise(in[which][u], divisor(sc));
+          if (s >= 0) reinterpret_cast<uint2*>(pool)[s * a.vecs + x] = codes;
         }
-        if (s >= 0) reinterpret_cast<uint4*>(pool)[s * a.vecs + x] = out;
       }
+      load(round + 1, u);  // on its way while the other vectors are worked on
     }
-    if (round + 1 < rounds) load(round + 1);
   }
 }
 
@@ -235,34 +258,42 @@ __device__ __forceinline__ uint2 dequantise4(uint32_t codes, float scale) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+__device__ __forceinline__ uint2 load_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 template <int FMT>
-__global__ void __launch_bounds__(kMoveThreads) cache_read_kernel(const MoveArgs a) {
-  constexpr int V = kVec<FMT>;
-  constexpr int U = 2;
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_read_kernel(const MoveArgs a) {
+  constexpr int U = 4;  // vectors of K and of V in flight per thread
   __shared__ long long slot[kMaxTokensPerCta];
   const CacheGeometry& g = a.g;
   const int t0 = blockIdx.x * a.tokens;
   const int nt = min(a.tokens, g.total_tokens - t0);
   const int items = nt * a.vecs;
   find_slots(g, a.starts, t0, nt, slot);
+  using Vec = std::conditional_t<FMT == kBf16, uint4, uint2>;
   for (int i0 = threadIdx.x; i0 < items; i0 += U * kMoveThreads) {
-    uint4 in[2][U];
+    Vec in[2][U];
     float sc[2][U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kMoveThreads;
       if (i >= items) break;
-      const int t = i / a.vecs, x = i - t * a.vecs;
+      const int t = __umulhi(i, a.vecs_inv), x = i - t * a.vecs;
       const long long s = slot[t];
-      const int head = x / (128 / V);
+      const int head = x >> 4;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const uint8_t* pool = which ? g.v_pool : g.k_pool;
         const float* scales = which ? g.v_scale : g.k_scale;
-        in[which][u] = make_uint4(0, 0, 0, 0);
+        in[which][u] = Vec{};
         sc[which][u] = 0.f;
         if (s >= 0) {
-          in[which][u] = load_stream(reinterpret_cast<const uint4*>(pool) + s * a.vecs + x);
+          const Vec* p = reinterpret_cast<const Vec*>(pool) + s * a.vecs + x;
+          if constexpr (FMT == kBf16) in[which][u] = load_stream(p);
+          else in[which][u] = load_stream8(p);
           if constexpr (FMT == kHeadScale) sc[which][u] = __ldg(scales + head);
           if constexpr (FMT == kTokenScale) sc[which][u] = __ldg(scales + scale_index(g, s, head));
         }
@@ -272,21 +303,18 @@ __global__ void __launch_bounds__(kMoveThreads) cache_read_kernel(const MoveArgs
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kMoveThreads;
       if (i >= items) break;
-      const int t = i / a.vecs, x = i - t * a.vecs;
+      const int t = __umulhi(i, a.vecs_inv), x = i - t * a.vecs;
       if (slot[t] == kSkip) continue;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        uint8_t* dst = const_cast<uint8_t*>(which ? a.v : a.k) + (t0 + t) * (which ? a.v_stride : a.k_stride) +
-                       (long long)x * (V * 2);
-        const uint4 c = in[which][u];
+        uint8_t* dst =
+            const_cast<uint8_t*>(which ? a.v : a.k) + (t0 + t) * (which ? a.v_stride : a.k_stride) + x * 16;
         if constexpr (FMT == kBf16) {
-          *reinterpret_cast<uint4*>(dst) = c;
+          *reinterpret_cast<uint4*>(dst) = in[which][u];
         } else {
           const float f = sc[which][u];
-          const uint2 p0 = dequantise4(c.x, f), p1 = dequantise4(c.y, f), p2 = dequantise4(c.z, f),
-                      p3 = dequantise4(c.w, f);
-          reinterpret_cast<uint4*>(dst)[0] = make_uint4(p0.x, p0.y, p1.x, p1.y);
-          reinterpret_cast<uint4*>(dst)[1] = make_uint4(p2.x, p2.y, p3.x, p3.y);
+          const uint2 lo = dequantise4(in[which][u].x, f), hi = dequantise4(in[which][u].y, f);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
       }
     }
@@ -368,8 +396,8 @@ __global__ void __launch_bounds__(kMoveThreads)
   if (threadIdx.x == 0) new_lens[r] = base + num;
 }
 
-// Tokens per CTA: as many as leave every SM eight CTAs (its 2048 threads), up
-// to the slots' array, so that one token's chain of lookups serves many vectors.
+// Tokens per CTA: as few as fill the SMs' CTAs at most once, and up to the slots' array, so that one token's chain of lookups
+// serves many vectors. (One fewer left a second wave of a few CTAs.)
 MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k, long long k_stride, const void* v,
                    long long v_stride) {
   MoveArgs a;
@@ -379,9 +407,10 @@ MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k,
   a.v = static_cast<const uint8_t*>(v);
   a.k_stride = k_stride * 2;
   a.v_stride = v_stride * 2;
-  a.vecs = g.Hkv * g.d / (g.e4m3 ? 16 : 8);
-  const int per = g.total_tokens / (148 * 8);
-  a.tokens = per < 1 ? 1 : (per > kMaxTokensPerCta ? kMaxTokensPerCta : per);
+  a.vecs = g.Hkv * g.d / kVec;
+  a.vecs_inv = (uint32_t)(((1ull << 32) + a.vecs - 1) / a.vecs);
+  const int ctas = 148 * kMoveCtas, per = (int)(((long long)g.total_tokens + ctas - 1) / ctas);
+  a.tokens = per > kMaxTokensPerCta ? kMaxTokensPerCta : per;
   return a;
 }
 
