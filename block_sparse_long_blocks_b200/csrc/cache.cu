@@ -22,7 +22,11 @@ using namespace packed;
 
 namespace {
 
-constexpr int kMoveThreads = 256, kMoveCtas = 5;  // CTAs per SM (48 registers a thread)
+constexpr int kMoveThreads = 256;
+// CTAs per SM and vectors of K and of V in flight per thread: writing computes, and takes more warps (a chunk of
+// whole prompts, e4m3: 220 us with 8 CTAs of one vector, 242 us with 5 of two); reading takes more loads each
+// (213 us with 5 of four, 294 us with 8, whose registers spill).
+constexpr int kWriteCtas = 8, kWriteVecs = 1, kReadCtas = 5, kReadVecs = 4;
 constexpr int kMaxTokensPerCta = 64;
 enum Format { kBf16 = 0, kHeadScale = 1, kTokenScale = 2 };
 
@@ -133,6 +137,8 @@ __device__ __forceinline__ Divisor divisor(float scale) {
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990): three packed instructions for two elements. The general division took
 // about twelve each and set the pace (4.2 of the 6.5 TB/s).
+// BOUNDED: no |x| exceeds 448 s.
+template <bool BOUNDED>
 __device__ __forceinline__ uint2 quantise(const uint4& in, const Divisor& d) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
   uint32_t code[4];
@@ -147,9 +153,10 @@ __device__ __forceinline__ uint2 quantise(const uint4& in, const Divisor& d) {
       float pa, pb;
       f2_unpack(q, pa, pb);
       f2_unpack(f2_fma(f2_fma(q, ns, x), y, q), qa, qb);
-      // (far beyond the largest code the estimate does, and the correction may overflow)
-      qa = fabsf(pa) < 1024.f ? qa : pa;
-      qb = fabsf(pb) < 1024.f ? qb : pb;
+      if constexpr (!BOUNDED) {  // far beyond the largest code the estimate does, and the correction may overflow
+        qa = fabsf(pa) < 1024.f ? qa : pa;
+        qb = fabsf(pb) < 1024.f ? qb : pb;
+      }
     } else {
       qa = __fdiv_rn(a, d.scale);
       qb = __fdiv_rn(b, d.scale);
@@ -192,8 +199,8 @@ __device__ __forceinline__ long long scale_index(const CacheGeometry& g, long lo
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_write_kernel(const MoveArgs a) {
-  constexpr int U = 2;  // vectors of K and of V in flight per thread
+__global__ void __launch_bounds__(kMoveThreads, kWriteCtas) cache_write_kernel(const MoveArgs a) {
+  constexpr int U = kWriteVecs;
   __shared__ long long slot[kMaxTokensPerCta];
   const CacheGeometry& g = a.g;
   const int t0 = blockIdx.x * a.tokens;
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_write_kernel(co
           } else {
             sc = __ldg(scales + head);
           }
-          const uint2 codes = quantise(in[which][u], divisor(sc));
+          const uint2 codes = quantise<FMT == kTokenScale>(in[which][u], divisor(sc));
           if (s >= 0) reinterpret_cast<uint2*>(pool)[s * a.vecs + x] = codes;
         }
       }
@@ -265,8 +272,8 @@ __device__ __forceinline__ uint2 load_stream8(const void* p) {
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_read_kernel(const MoveArgs a) {
-  constexpr int U = 4;  // vectors of K and of V in flight per thread
+__global__ void __launch_bounds__(kMoveThreads, kReadCtas) cache_read_kernel(const MoveArgs a) {
+  constexpr int U = kReadVecs;
   __shared__ long long slot[kMaxTokensPerCta];
   const CacheGeometry& g = a.g;
   const int t0 = blockIdx.x * a.tokens;
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 // Tokens per CTA: as few as fill the SMs' CTAs at most once, and up to the slots' array, so that one token's chain of lookups
 // serves many vectors. (One fewer left a second wave of a few CTAs.)
 MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k, long long k_stride, const void* v,
-                   long long v_stride) {
+                   long long v_stride, int ctas_per_sm) {
   MoveArgs a;
   a.g = g;
   a.starts = starts;
@@ -409,7 +416,7 @@ MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k,
   a.v_stride = v_stride * 2;
   a.vecs = g.Hkv * g.d / kVec;
   a.vecs_inv = (uint32_t)(((1ull << 32) + a.vecs - 1) / a.vecs);
-  const int ctas = 148 * kMoveCtas, per = (int)(((long long)g.total_tokens + ctas - 1) / ctas);
+  const int ctas = 148 * ctas_per_sm, per = (int)(((long long)g.total_tokens + ctas - 1) / ctas);
   a.tokens = per > kMaxTokensPerCta ? kMaxTokensPerCta : per;
   return a;
 }
@@ -418,7 +425,7 @@ MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k,
 
 cudaError_t launch_cache_write(const CacheGeometry& g, const void* k, long long k_stride, const void* v,
                                long long v_stride, cudaStream_t s) {
-  const MoveArgs a = move_args(g, nullptr, k, k_stride, v, v_stride);
+  const MoveArgs a = move_args(g, nullptr, k, k_stride, v, v_stride, kWriteCtas);
   const int grid = (g.total_tokens + a.tokens - 1) / a.tokens;
   if (!g.e4m3) cache_write_kernel<kBf16><<<grid, kMoveThreads, 0, s>>>(a);
   else if (g.token_scale) cache_write_kernel<kTokenScale><<<grid, kMoveThreads, 0, s>>>(a);
@@ -428,7 +435,7 @@ cudaError_t launch_cache_write(const CacheGeometry& g, const void* k, long long 
 
 cudaError_t launch_cache_read(const CacheGeometry& g, const int32_t* starts, void* k, long long k_stride, void* v,
                               long long v_stride, cudaStream_t s) {
-  const MoveArgs a = move_args(g, starts, k, k_stride, v, v_stride);
+  const MoveArgs a = move_args(g, starts, k, k_stride, v, v_stride, kReadCtas);
   const int grid = (g.total_tokens + a.tokens - 1) / a.tokens;
   if (!g.e4m3) cache_read_kernel<kBf16><<<grid, kMoveThreads, 0, s>>>(a);
   else if (g.token_scale) cache_read_kernel<kTokenScale><<<grid, kMoveThreads, 0, s>>>(a);
