@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   axis.build(a, warp_sum);  // (its barrier publishes the initialisation above)
   const int total = axis.total();
-  const int share = share_of(total, a.grid);
+  const int share = share_of(a, total);
   const long long x_first = (long long)blockIdx.x * share;
   if (x_first >= total) return;
   const int x_begin = (int)x_first, x_end = min(total, x_begin + share);
@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int r = axis.request_of(x_begin);
     for (int x = x_begin; x < x_end && ok;) {
-      const Segment sg = segment_at(a, axis, x, x_end, r);
+      Segment sg;
+      if (!next_segment(a, axis, x, x_end, r, sg)) continue;
       const int32_t* row = g.table + (long long)sg.r * g.max_pages;
       auto page_at = [&](int tile) {  // the page of this lane's part of a tile
         const int tok = tile * C::TILE + lane * sub_rows;
@@ -247,7 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      x += sg.t1 - sg.t0;
     }
     // every copy lands before the CTA's shared memory is released
     if (lane == 0) {
@@ -296,9 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
   int r = axis.request_of(x_begin);
   int segment = 0;
-  for (int x = x_begin; x < x_end; ++segment) {
-    const Segment sg = segment_at(a, axis, x, x_end, r);
-    x += sg.t1 - sg.t0;
+  for (int x = x_begin; x < x_end;) {
+    Segment sg;
+    if (!next_segment(a, axis, x, x_end, r, sg)) continue;
     const int nrows = sg.n * a.G;
     // ---- Q to shared memory, as the rows of A tiles
     if constexpr (!E4M3) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = i / (D / 8), gran = i % (D / 8), rho = sg.row0 + row;
         uint4 w = make_uint4(0, 0, 0, 0);
         if (row < C::ROWS && rho < nrows) {
-          const int t = rho / a.G, h = rho - t * a.G;
+          const int t = group_of(a, rho), h = rho - t * a.G;
           w = __ldg(reinterpret_cast<const uint4*>(a.q + (long long)(sg.off + t) * a.q_stride +
                                                    (sg.head * a.G + h) * D) + gran);
         }
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < EL / 2; ++i) w[i] = 0;
       if (rho < nrows) {
-        const int t = rho / a.G, h = rho - t * a.G;
+        const int t = group_of(a, rho), h = rho - t * a.G;
         const __nv_bfloat16* qp = a.q + (long long)(sg.off + t) * a.q_stride + (sg.head * a.G + h) * D + part * EL;
 #pragma unroll
         for (int i = 0; i < EL / 4; ++i) {
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < NB; ++b) {
       const int rho = sg.row0 + gr + 8 * b;
       in[b] = rho < nrows;
-      tok[b] = in[b] ? rho / a.G : 0;
+      tok[b] = in[b] ? group_of(a, rho) : 0;
       sl2[b] = s_scale[gr + 8 * b];
     }
     float v_mul = 1.f;  // what O is multiplied by at the end
@@ -737,8 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc.w += y.w;
         }
         const int d = round * C::RED_COLS + col;
-        const int t = row / a.G, h = row - t * a.G;
-        if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, t, d, C::TILE, acc);
+        const int t = group_of(a, row), h = row - t * a.G;
+        if (odd) {
+          float2 lo = make_float2(acc.x, acc.y), hi = make_float2(acc.z, acc.w);
+          add_odd_values<E4M3, TOKEN, D>(a, sg, t, d, C::TILE, lo);
+          add_odd_values<E4M3, TOKEN, D>(a, sg, t, d + 2, C::TILE, hi);
+          acc = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
         if (whole) {
           *reinterpret_cast<uint2*>(a.o + ((long long)(sg.off + t) * a.Hq + sg.head * a.G + h) * D + d) =
               make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));
@@ -748,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       consumers_sync();  // the next round, or the next segment's Q, may be written
     }
+    ++segment;
   }
 }
 
@@ -787,9 +793,9 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (sp.n == 0 || token < sp.off || token >= sp.off + sp.n) return;
   const int nt = tiles_of(a, sp), head = hq / a.G, row = (token - sp.off) * a.G + hq - head * a.G;
-  const int x0 = axis.first(r) + (head * units_of(a, sp) + (row >> a.rows_shift)) * nt, x1 = x0 + nt;
-  const int share = share_of(total, a.grid);
-  const int c0 = x0 / share, c1 = (x1 - 1) / share;
+  const int x0 = axis.first(r) + (head * units_of(a, sp) + (row >> a.rows_shift)) * (a.lead + nt), x1 = x0 + a.lead + nt;
+  const int share = share_of(a, total);
+  const int c0 = (x0 + a.lead) / share, c1 = (x1 - 1) / share;
   if (c0 == c1) return;  // one CTA had the whole unit and finished it
   const int lr = row & (a.rows - 1);
   // its partial in CTA c: the CTA's first segment, unless the unit begins inside the CTA's share
@@ -865,6 +871,9 @@ int sm_count() {
 // Rows per unit: the kernel here holds 8 or 16, the one for many rows (tree_wide.cu) one or two M-tiles of 128.
 int unit_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 128 ? 128 : 256; }
 
+// What a segment takes beside its tiles, in tiles.
+constexpr int kNarrowLead = 2, kWideLead = 6;
+
 int log2_of(int x) {
   int s = 0;
   while ((1 << s) < x) ++s;
@@ -924,6 +933,7 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   a.mask = t.mask;
   a.mask_words = t.mask_words;
   a.q = static_cast<const __nv_bfloat16*>(q);
+  a.G_inv = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
   a.q_stride = t.q_stride ? t.q_stride : (long long)t.hq * g.d;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
@@ -931,6 +941,8 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   a.scale_log2 = (float)(scale * 1.4426950408889634);
   a.grid = sm_count();  // (at most 256: the combining kernel's registers)
   a.tile = a.rows <= 16 ? kTileBytes / (g.d * (g.e4m3 ? 1 : 2)) : 128;
+  a.lead = a.rows <= 16 ? kNarrowLead : kWideLead;
+  a.min_share = a.rows <= 16 ? 1 : 2;
   a.rows_shift = log2_of(a.rows);
   a.tile_shift = log2_of(a.tile);
   const size_t rows = (size_t)2 * a.grid * a.rows;

@@ -23,9 +23,12 @@ constexpr float kSlack = 7.f, kShift = 8.f;
 struct TreeArgs {
   CacheGeometry g;
   int Hq, G;
+  uint32_t G_inv;         // ceil(2^32 / G)
   int max_tokens;
   int rows, rows_shift;   // rows per unit, a power of two
   int tile, tile_shift;   // keys per tile, a power of two
+  int lead;               // places on the axis before a unit's tiles: what a segment costs beside them, in tiles
+  int min_share;          // places of a CTA at least
   const uint32_t* mask;
   int mask_words;
   const __nv_bfloat16* q;
@@ -41,6 +44,10 @@ struct TreeArgs {
 // ---------------------------------------------------------------------------
 // the axis of tiles
 // ---------------------------------------------------------------------------
+// Every unit takes `lead` places and then one per key tile. The CTAs' shares are
+// equal runs of places, so that many short units are spread as evenly as the
+// tiles of a few long ones (28 rows over five requests, one of 14 tokens: the
+// CTA that got all heads of the short one took twice as long as the others).
 // Where a request's rows and keys lie (n = 0: empty, or rejected).
 struct Span {
   int off, n, kv;
@@ -72,7 +79,7 @@ constexpr int kSpanTable = 1024;
 __host__ __device__ constexpr int axis_bytes(int R) { return (R + 1) * (R <= kSpanTable ? 16 : 4); }
 constexpr int kAxisBytesMax = axis_bytes(kSpanTable) > axis_bytes(4096) ? axis_bytes(kSpanTable) : axis_bytes(4096);
 
-// The requests along the axis: first tile of each, and its span.
+// The requests along the axis: first place of each, and its span.
 struct Axis {
   int* mem;  // axis_bytes(R) of shared memory, 16-byte aligned
   int R;
@@ -105,7 +112,7 @@ struct Axis {
         int mine = 0;
         if (r < R) {
           s = load_span(a, r);
-          mine = tiles_of(a, s) * units_of(a, s) * a.g.Hkv;
+          mine = s.n == 0 ? 0 : (a.lead + tiles_of(a, s)) * units_of(a, s) * a.g.Hkv;
         }
         int incl = mine;
 #pragma unroll
@@ -132,7 +139,7 @@ struct Axis {
     __syncthreads();
   }
 
-  // The request whose tiles hold tile x (0 <= x < total).
+  // The request that place x belongs to (0 <= x < total).
   __device__ __forceinline__ int request_of(int x) const {
     int lo = 0, hi = R - 1;
     while (lo < hi) {
@@ -144,7 +151,21 @@ struct Axis {
   }
 };
 
-__device__ __forceinline__ int share_of(int total, int grid) { return (total + grid - 1) / grid; }
+// row / G, for rows below 2^16
+__device__ __forceinline__ int group_of(const TreeArgs& a, int row) {
+  return a.G == 1 ? row : (int)__umulhi((uint32_t)row, a.G_inv);
+}
+// x / y for 0 <= x, 0 < y: below 2^20 the float32 quotient (off by 2^-22 of it) is wrong by one at most.
+__device__ __forceinline__ int quotient(int x, int y) {
+  if (x >= 1 << 20 || y >= 1 << 20) return x / y;
+  int q = (int)__fdividef((float)x, (float)y);
+  const int rest = x - q * y;
+  return rest < 0 ? q - 1 : rest >= y ? q + 1 : q;
+}
+
+__device__ __forceinline__ int share_of(const TreeArgs& a, int total) {
+  return max((total + a.grid - 1) / a.grid, a.min_share);
+}
 
 // One run of tiles of one unit within a CTA's share.
 struct Segment {
@@ -154,22 +175,25 @@ struct Segment {
   __device__ __forceinline__ bool whole() const { return t1 - t0 == nt; }
 };
 
-__device__ __forceinline__ Segment segment_at(const TreeArgs& a, const Axis& axis, int x, int end, int& r) {
+// The segment that begins at place x of a share that ends at `end`; x goes on
+// behind it. False if its places hold no tile.
+__device__ __forceinline__ bool next_segment(const TreeArgs& a, const Axis& axis, int& x, int end, int& r, Segment& s) {
   while (axis.first(r + 1) <= x) ++r;
   const Span sp = axis.span(a, r);
-  Segment s;
   s.r = r;
   s.off = sp.off;
   s.n = sp.n;
   s.kv = sp.kv;
   s.nt = tiles_of(a, sp);
   s.base = s.kv - s.n;
-  const int nm = units_of(a, sp), y = x - axis.first(r), unit = y / s.nt;
-  s.t0 = y - unit * s.nt;
-  s.t1 = min(s.nt, s.t0 + (end - x));
-  s.head = nm == 1 ? unit : unit / nm;
+  const int nm = units_of(a, sp), y = x - axis.first(r), len = a.lead + s.nt, unit = quotient(y, len);
+  const int u0 = y - unit * len, u1 = min(len, u0 + (end - x));
+  s.t0 = max(u0 - a.lead, 0);
+  s.t1 = max(u1 - a.lead, 0);
+  s.head = quotient(unit, nm);
   s.row0 = (unit - s.head * nm) * a.rows;
-  return s;
+  x += u1 - u0;
+  return s.t1 > s.t0;
 }
 
 // Which of the 32 positions from pos0 on a row of token `tok` sees, as bits (`in`: the row exists).
@@ -240,10 +264,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Infinities and NaN that new tokens of this segment hold in four columns of V
+// Infinities and NaN that new tokens of this segment hold in two columns of V
 // reach the rows that see them (rare: they entered the products as zeros).
 template <bool E4M3, bool TOKEN, int D>
-__device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg, int t, int d, int tile, float4& acc) {
+__device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg, int t, int d, int tile, float2& acc) {
   const CacheGeometry& g = a.g;
   const int32_t* row = g.table + (long long)sg.r * g.max_pages;
   for (int pos = max(sg.base, sg.t0 * tile); pos < min(sg.kv, sg.t1 * tile); ++pos) {
@@ -253,24 +277,21 @@ __device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg
     if (!see || page < 0 || page >= g.num_pages) continue;
     const long long slot = ((long long)page << g.page_shift) + (pos & (g.page_size - 1));
     const long long at = (slot * g.Hkv + sg.head) * D + d;
-    float v[4];
+    float2 v;
     if constexpr (E4M3) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(g.v_pool + at);
-      float sc = 1.f;
-      if (TOKEN) sc = __ldg(g.v_scale + (((long long)page * g.Hkv + sg.head) << g.page_shift) + (pos & (g.page_size - 1)));
-      const __half2_raw lo = {(unsigned short)widen_lo(w), (unsigned short)(widen_lo(w) >> 16)};
-      const __half2_raw hi = {(unsigned short)widen_hi(w), (unsigned short)(widen_hi(w) >> 16)};
-      const float2 x = __half22float2(__half2(lo)), y = __half22float2(__half2(hi));
-      v[0] = x.x * sc, v[1] = x.y * sc, v[2] = y.x * sc, v[3] = y.y * sc;
+      const uint32_t w = widen_lo(*reinterpret_cast<const uint16_t*>(g.v_pool + at));
+      v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      if (TOKEN) {
+        const float sc = __ldg(g.v_scale + (((long long)page * g.Hkv + sg.head) << g.page_shift) + (pos & (g.page_size - 1)));
+        v.x *= sc;
+        v.y *= sc;
+      }
     } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(g.v_pool + at * 2);
-      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
-      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(g.v_pool + at * 2);
+      v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    if (!isfinite(v[0])) acc.x += v[0];
-    if (!isfinite(v[1])) acc.y += v[1];
-    if (!isfinite(v[2])) acc.z += v[2];
-    if (!isfinite(v[3])) acc.w += v[3];
+    if (!isfinite(v.x)) acc.x += v.x;
+    if (!isfinite(v.y)) acc.y += v.y;
   }
 }
 

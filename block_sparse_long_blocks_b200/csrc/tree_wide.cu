@@ -83,13 +83,30 @@ struct Cfg {
                                                         // of a warpgroup to its next
   static constexpr int NUM_BARS = 2 * K_SLOTS + 2 * V_SLOTS + 2 * M_SLOTS + 2 + 2 + 4 + 2 + 6;
   static constexpr int SMEM_FIXED = 1024 + Q + (K_SLOTS + V_SLOTS) * LOAD + W_SLOTS * TILE +
-                                    (E4M3 ? kScales * 2 * kKeys * 4 : 0) + 128 * 16 + NUM_BARS * 8 + 336;
-  static constexpr int COLS = Q / 512 < D ? Q / 512 : D;  // columns of O per round in which two warpgroups' O meet
+                                    (E4M3 ? (kScales * 2 + 1) * kKeys * 4 : 0) + 256 * 16 + 1024 + NUM_BARS * 8 + 336;
+  // columns of O that either of two warpgroups hands the other through Q's place at a time
+  static constexpr int COLS = Q1 / 1024;
   static_assert(SMEM_FIXED + kAxisBytesMax <= 227 * 1024, "shared memory");
   static_assert(K_SLOTS % 2 == 0, "a slot is of one issuer");
-  static_assert(COLS % 32 == 0 && D % COLS == 0, "rounds of whole TMEM loads");
+  static_assert(PAIR || (COLS % 16 == 0 && D / 2 % COLS == 0), "rounds of whole TMEM loads");
 };
 
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Columns c .. c + 15 of TMEM lanes l .. l + 15 (taddr) as matrix fragments: element 4 j + e of a lane is row
+// lane / 4 + 8 (e / 2), column 8 j + 2 (lane % 4) + e % 2.
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, float* f) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <bool E4M3, bool TOKEN, int D, bool PAIR>
@@ -106,8 +123,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   uint8_t* sM = E4M3 ? sW : sV;                  // V tiles as multiplied
   float* s_ksc = reinterpret_cast<float*>(sW + C::W_SLOTS * C::TILE);  // [kScales][kKeys]
   float* s_vsc = s_ksc + (E4M3 ? kScales * kKeys : 0);
-  float4* s_half = reinterpret_cast<float4*>(s_vsc + (E4M3 ? kScales * kKeys : 0));  // [128] second warpgroup's sums
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(s_half + 128);
+  float* s_ones = s_vsc + (E4M3 ? kScales * kKeys : 0);                // [kKeys] (TOKEN)
+  float4* s_half = reinterpret_cast<float4*>(s_ones + (E4M3 ? kKeys : 0));  // [2][128] the warpgroups' sums
+  float* s_back = reinterpret_cast<float*>(s_half + 256);                   // [2][128] factors of Q's rows (e4m3)
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(s_back + 256);
   uint64_t* k_empty = k_full + C::K_SLOTS;
   uint64_t* v_full = k_empty + C::K_SLOTS;        // loaded
   uint64_t* v_empty = v_full + C::V_SLOTS;
@@ -131,7 +150,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   const CacheGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) {
+  if (TOKEN && threadIdx.x < kKeys) s_ones[threadIdx.x] = 1.f;
+  if (threadIdx.x == (kMmaWarp + 1) * 32) {  // (warp 0 has the axis to build)
     constexpr uint32_t issuers = PAIR ? 2 : 1;  // that multiply with a tile
     for (int s = 0; s < C::K_SLOTS; ++s) {
       mbar_init(k_full + s, 1);
@@ -154,8 +174,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       mbar_init(drain + w, 1);
       mbar_init(turn + w, 1);
     }
-    mbar_init(half_full, 128);
-    mbar_init(half_empty, 128);
+    mbar_init(half_full, 256);
+    mbar_init(half_empty, 256);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -168,7 +188,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = axis.total();
-  const int share = share_of(total, a.grid);
+  const int share = share_of(a, total);
   const long long x_first = (long long)blockIdx.x * share;
   if (x_first >= total) {
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
@@ -188,9 +208,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     const int sub_rows = min(g.page_size, kKeys), sub_max = kKeys / sub_rows;  // sub_max <= 8
     int kn = 0, vn = 0;  // K and V tiles issued
     for (int x = x_begin; x < x_end && ok;) {
-      const Segment sg = segment_at(a, axis, x, x_end, r);
+      Segment sg;
+      if (!next_segment(a, axis, x, x_end, r, sg)) continue;
       const int nt = sg.t1 - sg.t0;
-      x += nt;
       const int32_t* row = g.table + (long long)sg.r * g.max_pages;
       auto page_at = [&](int i) {  // the page of this lane's part of tile i of the segment
         const int tok = (sg.t0 + i) * kKeys + lane * sub_rows;
@@ -300,9 +320,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       int tn = 0, qn = 0, pn = 0, turns = 0;
       if (PAIR && w == 1) mbar_arrive(turn);  // the first turn is issuer 0's
       for (int x = x_begin; x < x_end && ok;) {
-        const Segment sg = segment_at(a, axis, x, x_end, r);
+        Segment sg;
+        if (!next_segment(a, axis, x, x_end, r, sg)) continue;
         const int nt = sg.t1 - sg.t0;
-        x += nt;
         const int first = PAIR ? 0 : (w - tn) & 1;  // tiles first, first + AHEAD, ...
         if (!wait(q_full + (PAIR ? w : 0), (uint32_t)qn & 1u)) break;
         ++qn;
@@ -350,10 +370,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     // ------------------------------------------------------------------ converters
     const int ct = threadIdx.x - L::CONVERT_WARP * 32, cw = warp - L::CONVERT_WARP;
     int tn = 0, segment = 0;
-    for (int x = x_begin; x < x_end && ok; ++segment) {
-      const Segment sg = segment_at(a, axis, x, x_end, r);
+    for (int x = x_begin; x < x_end && ok;) {
+      Segment sg;
+      if (!next_segment(a, axis, x, x_end, r, sg)) continue;
       const int nt = sg.t1 - sg.t0;
-      x += nt;
       bool fresh = true;  // the segment's flag is not cleared yet
       auto flag_odd = [&](bool odd) {
         volatile int* f = s_odd + segment % kFlags * 4 + cw;
@@ -395,7 +415,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
                                FP_DEV_TIMEOUT);
           if (!ok) break;
           const uint8_t* src = sV + vs * C::LOAD;
-#pragma unroll
+#pragma unroll 4
           for (int q = ct; q < kKeys * 8; q += L::CONVERTERS) {
             const int key = q >> 3, g8 = q & 7, sw = key & 7;
             uint4 w = *reinterpret_cast<const uint4*>(src + key * 128 + ((g8 ^ sw) << 4));
@@ -438,6 +458,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
         mbar_arrive(m_full + ms);
         if (E4M3) mbar_arrive(v_empty + vs);
       }
+      ++segment;
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax warpgroups
@@ -447,64 +468,86 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     const uint32_t tS = tmem + lane_base + w * 128;
     const uint32_t tO = tmem + lane_base + 256 + w * 128;
     int tn = 0, sn = 0, on = 0, hn = 0, segment = 0;
-    for (int x = x_begin; x < x_end; ++segment) {
-      const Segment sg = segment_at(a, axis, x, x_end, r);
+    for (int x = x_begin; x < x_end;) {
+      Segment sg;
+      if (!next_segment(a, axis, x, x_end, r, sg)) continue;
       const int nt = sg.t1 - sg.t0;
-      x += nt;
       const int lr = PAIR ? w * 128 + row : row, rho = sg.row0 + lr;
       const bool in = rho < sg.n * a.G;
-      const int tok = in ? rho / a.G : 0, h = in ? rho - tok * a.G : 0;
-      // ---- this thread's row of Q (of a shared tile: this warpgroup's chunk)
+      const int tok = in ? group_of(a, rho) : 0, h = in ? rho - tok * a.G : 0;
+      const int rows_in = __popc(__ballot_sync(0xffffffffu, in));  // (the warp's first ones)
+      // ---- Q: the rows that exist, with consecutive lanes on a row. (What stays in the others' place makes scores
+      // of rows that nobody stores.) Of a shared tile either warpgroup takes half of every row, or every other pair.
       float sl2 = a.scale_log2;
       {
-        const uint4* qp = reinterpret_cast<const uint4*>(a.q + (long long)(sg.off + tok) * a.q_stride +
-                                                         (sg.head * a.G + h) * D);
-        uint8_t* dst = sQ + (PAIR ? w * C::Q1 : 0) + row * 128;
+        const long long mine = in ? (long long)(sg.off + tok) * a.q_stride + (sg.head * a.G + h) * D : 0;
+        uint8_t* dst = sQ + (PAIR ? w * C::Q1 : 0);
         if constexpr (!E4M3) {
-#pragma unroll
-          for (int ch = 0; ch < C::CH; ++ch) {
-            if (!PAIR && ch != w) continue;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(dst + ch * kChunk + (((i ^ row) & 7) << 4)) =
-                  in ? __ldg(qp + ch * 8 + i) : make_uint4(0, 0, 0, 0);
-          }
-        } else {
-          uint4 v[16];
-          float mx = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[i] = in ? __ldg(qp + i) : make_uint4(0, 0, 0, 0);
-            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
-          }
-          // times 2^(7 - floor(log2 max)): the largest lies in [2^7, 2^8); rows of zeros or below 2^-100 take the limits
-          const int e2 = mx == 0.f ? 7 : max((int)((__float_as_uint(mx) >> 23) & 255u) - 127, -100);
-          const float up = mx < INFINITY ? __uint_as_float((uint32_t)(7 - e2 + 127) << 23) : __uint_as_float(0x7fc00000u);
-          sl2 *= __uint_as_float((uint32_t)(e2 - 7 + 127) << 23);
-          if (!TOKEN) sl2 *= __ldg(g.k_scale + sg.head);
-          if (sl2 == 0.f) sl2 = 1.2e-38f;  // (0 * -inf of a masked key would be NaN)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {  // 16 elements; of a shared tile the first warpgroup writes hi, the second lo
-            const uint32_t u[8] = {v[2 * i].x, v[2 * i].y, v[2 * i].z, v[2 * i].w,
-                                   v[2 * i + 1].x, v[2 * i + 1].y, v[2 * i + 1].z, v[2 * i + 1].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x0 = __uint_as_float(u[2 * e] << 16) * up, x1 = __uint_as_float(u[2 * e] & 0xffff0000u) * up;
-              const float x2 = __uint_as_float(u[2 * e + 1] << 16) * up;
-              const float x3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * up;
-              hi[e] = pack_codes(x0, x1) | (pack_codes(x2, x3) << 16);
-              const uint32_t h01 = widen_lo(hi[e]), h23 = widen_hi(hi[e]);
-              const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
-              const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-              lo[e] = pack_codes(x0 - f01.x, x1 - f01.y) | (pack_codes(x2 - f23.x, x3 - f23.y) << 16);
+          constexpr int PER = PAIR ? D / 8 : 8;  // granules of a row that this warpgroup copies
+          const int ch0 = PAIR ? 0 : w, gran = lane % PER;
+          if (ch0 < C::CH) {
+#pragma unroll 2
+            for (int rr = lane / PER; rr < 32; rr += 32 / PER) {
+              const long long q = __shfl_sync(0xffffffffu, mine, rr);
+              const int at = (warp & 3) * 32 + rr;
+              if (rr < rows_in)
+                copy_async16(dst + (ch0 + (gran >> 3)) * kChunk + at * 128 + (((gran ^ at) & 7) << 4),
+                             a.q + q + ch0 * 64 + gran * 8);
             }
-            uint8_t* at = dst + (((i ^ row) & 7) << 4);
-            if (PAIR || w == 0) *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (PAIR || w == 1) *reinterpret_cast<uint4*>(at + kChunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          copies_wait();
+        } else {
+          const int gran = lane & 15, step = PAIR ? 2 : 4, rr0 = (PAIR ? 0 : 2 * w) + (lane >> 4);
+          auto fetch = [&](int rr) {
+            const long long q = __shfl_sync(0xffffffffu, mine, rr & 31);
+            return rr < rows_in ? __ldg(reinterpret_cast<const uint4*>(a.q + q) + gran) : make_uint4(0, 0, 0, 0);
+          };
+          uint4 next[2] = {fetch(rr0), fetch(rr0 + step)};
+#pragma unroll 1
+          for (int rr = rr0; rr - (lane >> 4) < rows_in; rr += 2 * step) {
+            const uint4 v[2] = {next[0], next[1]};
+            next[0] = fetch(rr + 2 * step);
+            next[1] = fetch(rr + 3 * step);
+            float mx[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                mx[k] = max3(mx[k], fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+              // times 2^(7 - floor(log2 max)): the largest lies in [2^7, 2^8); rows of zeros or below 2^-100 take the
+              // limits
+              const int e2 = mx[k] == 0.f ? 7 : max((int)((__float_as_uint(mx[k]) >> 23) & 255u) - 127, -100);
+              const float up =
+                  mx[k] < INFINITY ? __uint_as_float((uint32_t)(7 - e2 + 127) << 23) : __uint_as_float(0x7fc00000u);
+              uint32_t hi[2], lo[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float x0 = __uint_as_float(u[2 * e] << 16) * up, x1 = __uint_as_float(u[2 * e] & 0xffff0000u) * up;
+                const float x2 = __uint_as_float(u[2 * e + 1] << 16) * up;
+                const float x3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * up;
+                hi[e] = pack_codes(x0, x1) | (pack_codes(x2, x3) << 16);
+                const uint32_t h01 = widen_lo(hi[e]), h23 = widen_hi(hi[e]);
+                const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+                const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+                lo[e] = pack_codes(x0 - f01.x, x1 - f01.y) | (pack_codes(x2 - f23.x, x3 - f23.y) << 16);
+              }
+              const int r1 = rr + k * step, at = (warp & 3) * 32 + r1;
+              if (r1 < rows_in) {
+                uint8_t* put = dst + at * 128 + ((((gran >> 1) ^ at) & 7) << 4) + (gran & 1) * 8;
+                *reinterpret_cast<uint2*>(put) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(put + kChunk) = make_uint2(lo[0], lo[1]);
+                if (gran == 0) s_back[(PAIR ? w * 128 : 0) + at] = __uint_as_float((uint32_t)(e2 - 7 + 127) << 23);
+              }
+            }
           }
         }
         fence_async();
@@ -517,55 +560,69 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       // divided, so that O stays an average of V rows whatever the rounding
       float ref = -INFINITY, l = 0.f, lu = 0.f;
       uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
+      const bool any_rows = __any_sync(0xffffffffu, in);
       const int first = PAIR ? 0 : (w - tn) & 1;
       for (int i = first; i < nt; i += C::AHEAD) {
         ok = mbar_wait<true>(s_full + w, (uint32_t)sn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
         if (!ok) break;
         ++sn;
         tc_fence_after();
+        if (E4M3 && i == first) {  // (the tile's rows are there: the product was made of them)
+          sl2 *= in ? s_back[(PAIR ? w * 128 : 0) + row] : 1.f;
+          if (!TOKEN) sl2 *= __ldg(g.k_scale + sg.head);
+          if (sl2 == 0.f) sl2 = 1.2e-38f;  // (0 * -inf of a masked key would be NaN)
+        }
+        if (!any_rows) {  // (what P holds for them goes to rows that nobody stores)
+          tc_fence_before();
+          mbar_arrive(p_full + 2 * w);
+          mbar_arrive(p_full + 2 * w + 1);
+          continue;
+        }
         const int pos0 = (sg.t0 + i) * kKeys;
-        float s[kKeys];
-        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-        {
-          uint32_t sr[kKeys];
-          tmem_ld32(tS, sr);
-          tmem_ld32(tS + 32, sr + 32);
+        const float* ksc = s_ksc + (tn + i) % kScales * kKeys;
+        if (pos0 + kKeys > sg.base) {
+          // New tokens, or slots behind the last one: the scores are scaled and masked where they lie.
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += 32) {
+            float x[32];
+            tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(x));
+            const uint32_t see = row_sees(a, sg, in, tok, pos0 + c0);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = (see >> c & 1u) ? (TOKEN ? x[c] * ksc[c0 + c] : x[c]) : -INFINITY;
+            tmem_st32(tS + c0, *reinterpret_cast<const uint32_t(*)[32]>(x));
+          }
+          tmem_wait_st();
+          ksc = s_ones;
+        }
+        // 64 scores from column c0 on. They are read twice, for the maximum and for the weights, in loops and not
+        // unrolled: a CTA that has two tiles of a unit runs this code twice, and instructions that are not in the
+        // cache yet take seven clocks each.
+        auto scores = [&](float* x, int c0) {
+          tmem_ld32(tS + c0, reinterpret_cast<uint32_t*>(x));
+          tmem_ld32(tS + c0 + 32, reinterpret_cast<uint32_t*>(x) + 32);
           tmem_wait_ld();
-          tmem_ld32(tS + 64, sr + 64);
-          tmem_ld32(tS + 96, sr + 96);
+          if constexpr (TOKEN) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            if (hf == 1) tmem_wait_ld();
-#pragma unroll
-            for (int c = hf * 64; c < (hf + 1) * 64; ++c) s[c] = __uint_as_float(sr[c]);
-            if constexpr (TOKEN) {
-              const float* sc = s_ksc + (tn + i) % kScales * kKeys;
-#pragma unroll
-              for (int c = hf * 64; c < (hf + 1) * 64; c += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(sc + c);
-                f2_unpack(f2_mul(f2_pack(s[c], s[c + 1]), f2_pack(f.x, f.y)), s[c], s[c + 1]);
-                f2_unpack(f2_mul(f2_pack(s[c + 2], s[c + 3]), f2_pack(f.z, f.w)), s[c + 2], s[c + 3]);
-              }
-            }
-            if (pos0 + kKeys > sg.base) {  // new tokens, or slots behind the last one
-#pragma unroll
-              for (int c0 = hf * 64; c0 < (hf + 1) * 64; c0 += 32) {
-                const uint32_t see = row_sees(a, sg, in, tok, pos0 + c0);
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!(see >> c & 1u)) s[c0 + c] = -INFINITY;
-              }
-            }
-#pragma unroll
-            for (int c = hf * 64; c < (hf + 1) * 64; c += 8) {
-              m0 = fmaxf(fmaxf(m0, s[c]), s[c + 1]);
-              m1 = fmaxf(fmaxf(m1, s[c + 2]), s[c + 3]);
-              m2 = fmaxf(fmaxf(m2, s[c + 4]), s[c + 5]);
-              m3 = fmaxf(fmaxf(m3, s[c + 6]), s[c + 7]);
+            for (int c = 0; c < 64; c += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(ksc + c0 + c);
+              f2_unpack(f2_mul(f2_pack(x[c], x[c + 1]), f2_pack(f.x, f.y)), x[c], x[c + 1]);
+              f2_unpack(f2_mul(f2_pack(x[c + 2], x[c + 3]), f2_pack(f.z, f.w)), x[c + 2], x[c + 3]);
             }
           }
+        };
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kKeys; c0 += 64) {
+          float x[64];
+          scores(x, c0);
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            m0 = max3(m0, x[c], x[c + 1]);
+            m1 = max3(m1, x[c + 2], x[c + 3]);
+          }
         }
-        const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+        const float mx = fmaxf(m0, m1) * sl2;
         float f = 1.f;
         if (mx > ref + kSlack) {
           f = exp2_fast(ref - mx);
@@ -607,34 +664,32 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
         uint64_t sum0 = 0, sum1 = 0, used0 = 0, used1 = 0;  // (pairs of float32 zeros)
         const float* vsc = s_vsc + (tn + i) % kScales * kKeys;
         // P goes out in two halves of the keys; O += P V starts on the first while the second is computed
-#pragma unroll
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
+          float x[64];
+          uint32_t p16[32];
+          scores(x, hf * 64);
 #pragma unroll
-          for (int c0 = hf * 64; c0 < (hf + 1) * 64; c0 += 32) {
-            uint32_t hi[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int c = c0 + 2 * e;
-              float p0, p1;
-              f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sl2x2, negx2), p0, p1);
-              p0 = exp2_fast(p0);
-              p1 = exp2_fast(p1);
-              const uint64_t p = f2_pack(p0, p1);
-              if (e & 1) sum1 = f2_add(sum1, p);
-              else sum0 = f2_add(sum0, p);
-              if constexpr (TOKEN) {
-                const float2 vs = *reinterpret_cast<const float2*>(vsc + c);
-                f2_unpack(f2_mul(f2_mul(p, f2_pack(vs.x, vs.y)), invx2), p0, p1);
-              }
-              hi[e] = pack2<E4M3>(p0, p1);
-              if constexpr (!E4M3) {
-                const uint64_t q = f2_pack(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u));
-                if (e & 1) used1 = f2_add(used1, q);
-                else used0 = f2_add(used0, q);
-              }
+          for (int e = 0; e < 32; ++e) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sl2x2, negx2), p0, p1);
+            p0 = exp2_fast(p0);
+            p1 = exp2_fast(p1);
+            const uint64_t p = f2_pack(p0, p1);
+            if (e & 1) sum1 = f2_add(sum1, p);
+            else sum0 = f2_add(sum0, p);
+            if constexpr (TOKEN) {
+              const float2 vs = *reinterpret_cast<const float2*>(vsc + hf * 64 + 2 * e);
+              f2_unpack(f2_mul(f2_mul(p, f2_pack(vs.x, vs.y)), invx2), p0, p1);
             }
-            tmem_st16(tS + c0 / 2, hi);
+            p16[e] = pack2<E4M3>(p0, p1);
+            if constexpr (!E4M3) {
+              const uint64_t q = f2_pack(__uint_as_float(p16[e] << 16), __uint_as_float(p16[e] & 0xffff0000u));
+              if (e & 1) used1 = f2_add(used1, q);
+              else used0 = f2_add(used0, q);
+            }
           }
+          tmem_st32(tS + hf * 32, p16);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_full + 2 * w + hf);
@@ -662,28 +717,26 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       const long long part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
       auto odd_values = [](volatile int* f) { return E4M3 ? (f[0] | f[1] | f[2] | f[3]) != 0 : f[0] != 0; };
       const bool odd = sg.t1 * kKeys > sg.base && odd_values(s_odd + segment % kFlags * 4);
-      auto store = [&](int d0, float* o) {  // columns d0 .. d0 + 31
-        if (!in) return;
-        if (odd) {
-#pragma unroll 1
-          for (int c = 0; c < 32; c += 4) {
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            add_odd_values<E4M3, TOKEN, D>(a, sg, tok, d0 + c, kKeys, acc);
+      const long long out = whole ? ((long long)(sg.off + tok) * a.Hq + sg.head * a.G + h) * D : (part * a.rows + lr) * D;
+      // This lane's fragment rows: lane / 4 + 8 k of the warp's.
+      const int fr = lane >> 2, fc = 2 * (lane & 3);
+      // O's columns c0 .. c0 + 15 of 16 rows (half hf), as fragments with their rows' factors applied, go out. A thread
+      // that stored its own row wrote 32 lines per store, which took 9000 clocks.
+      auto store16 = [&](const float* f, int hf, int c0) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              if (k == c) o[k] += acc.x, o[k + 1] += acc.y, o[k + 2] += acc.z, o[k + 3] += acc.w;
+        for (int k = 0; k < 2; ++k) {
+          const int rr = hf * 16 + 8 * k + fr;
+          const long long to = __shfl_sync(0xffffffffu, out, rr) + c0 + fc;
+          const int t = odd ? __shfl_sync(0xffffffffu, tok, rr) : 0;
+          if (rr < rows_in) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float2 v = make_float2(f[4 * j + 2 * k], f[4 * j + 2 * k + 1]);
+              if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, t, c0 + 8 * j + fc, kKeys, v);
+              if (whole) *reinterpret_cast<uint32_t*>(a.o + to + 8 * j) = pack2<false>(v.x, v.y);
+              else *reinterpret_cast<float2*>(a.part_o + to + 8 * j) = v;
+            }
           }
-        }
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o + ((long long)(sg.off + tok) * a.Hq + sg.head * a.G + h) * D + d0);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            dst[c] = make_uint4(pack2<false>(o[8 * c], o[8 * c + 1]), pack2<false>(o[8 * c + 2], o[8 * c + 3]),
-                                pack2<false>(o[8 * c + 4], o[8 * c + 5]), pack2<false>(o[8 * c + 6], o[8 * c + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + (part * a.rows + lr) * D + d0);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
       };
       auto store_lse = [&](float top, float sum) {
@@ -695,66 +748,86 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           a.lse[(long long)(sg.head * a.G + h) * g.total_tokens + sg.off + tok] = lse2 * 0.69314718055994531f;
       };
       if (PAIR || nt == 1) {
-        if (PAIR || first == 0) {
+        if ((PAIR || first == 0) && any_rows) {
           const float f = lu == 0.f ? 0.f : v_mul / lu;
 #pragma unroll 1
-          for (int d0 = 0; d0 < D; d0 += 32) {
-            uint32_t o[32];
-            float of[32];
-            tmem_ld32(tO + d0, o);
-            tmem_wait_ld();
+          for (int hf = 0; hf < 2; ++hf) {
+            if (hf * 16 >= rows_in) break;
+            const float f0 = __shfl_sync(0xffffffffu, f, hf * 16 + fr), f1 = __shfl_sync(0xffffffffu, f, hf * 16 + 8 + fr);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              float o[16];
+              tmem_ld_frag16(tO + (hf << 20) + c0, o);
+              tmem_ld_frag16(tO + (hf << 20) + c0 + 16, o + 8);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) of[c] = f == 0.f ? 0.f : __uint_as_float(o[c]) * f;
-            store(d0, of);
+              for (int e = 0; e < 16; ++e) o[e] *= (e & 2) ? f1 : f0;
+              store16(o, hf, c0);
+              store16(o + 8, hf, c0 + 16);
+            }
           }
           store_lse(ref, l);
         }
       } else {
-        // the second warpgroup's part goes through Q's place (its products are over) in rounds of COLS columns
-        float* buf = reinterpret_cast<float*>(sQ);  // [COLS][128]
-        if (w == 1) s_half[row] = make_float4(ref, l, v_mul, lu);
-        float f0 = 0.f, f1 = 0.f, top = 0.f, sum = 0.f;
+        // Either warpgroup finishes half of the columns: the other's O comes through Q's place (its products are over)
+        // in rounds of COLS columns, every thread's fragments to the same thread of the other.
+        s_half[w * 128 + row] = make_float4(ref, l, v_mul, lu);
+        float* box = reinterpret_cast<float*>(sQ) + (threadIdx.x & 127) * 4;  // [2][COLS / 4 pieces][128][4]
+        constexpr int PIECES = C::COLS / 4;
+        float top = 0.f, sum = 0.f, mine = 0.f, theirs = 0.f;
+        float fm[4], ft[4];  // factors of this lane's rows
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += C::COLS) {
-          if (w == 1) {
-#pragma unroll 1
-            for (int d0 = 0; d0 < C::COLS; d0 += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c0 + d0, o);
-              tmem_wait_ld();
+        for (int c0 = 0; c0 < D / 2; c0 += C::COLS) {
+          const int give = (1 - w) * (D / 2) + c0, keep = w * (D / 2) + c0;
+          if (any_rows) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) buf[(d0 + c) * 128 + row] = __uint_as_float(o[c]);
-            }
-            mbar_arrive(half_full);
-          } else {
-            ok = mbar_wait<true>(half_full, (uint32_t)hn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
-            if (!ok) break;
-            if (c0 == 0) {
-              const float4 y = s_half[row];
-              top = fmaxf(ref, y.x);
-              const float e0 = top == -INFINITY ? 1.f : exp2_fast(ref - top);
-              const float e1 = top == -INFINITY ? 1.f : exp2_fast(y.x - top);
-              sum = l * e0 + y.y * e1;
-              const float used = lu * e0 + y.w * e1;
-              f0 = used == 0.f ? 0.f : e0 * v_mul / used;
-              f1 = used == 0.f ? 0.f : e1 * y.z / used;
-            }
-#pragma unroll 1
-            for (int d0 = 0; d0 < C::COLS; d0 += 32) {
-              uint32_t o[32];
-              float of[32];
-              tmem_ld32(tO + c0 + d0, o);
-              tmem_wait_ld();
+            for (int c = 0; c < C::COLS; c += 16)
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const float y = buf[(d0 + c) * 128 + row];
-                of[c] = (f0 == 0.f ? 0.f : __uint_as_float(o[c]) * f0) + (f1 == 0.f ? 0.f : y * f1);
+              for (int hf = 0; hf < 2; ++hf) {
+                float o[8];
+                tmem_ld_frag16(tO + (hf << 20) + give + c, o);
+                tmem_wait_ld();
+                float* at = box + ((1 - w) * PIECES + c / 4 + hf * 2) * 512;
+                *reinterpret_cast<float4*>(at) = make_float4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<float4*>(at + 512) = make_float4(o[4], o[5], o[6], o[7]);
               }
-              store(c0 + d0, of);
-            }
-            mbar_arrive(half_empty);
           }
-          // both go on when the buffer is read: it is filled again, or with the next segment's Q
+          mbar_arrive(half_full);
+          ok = mbar_wait<true>(half_full, (uint32_t)hn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
+          if (!ok) break;
+          if (c0 == 0) {
+            const float4 y = s_half[(1 - w) * 128 + row];
+            top = fmaxf(ref, y.x);
+            const float e0 = top == -INFINITY ? 1.f : exp2_fast(ref - top);
+            const float e1 = top == -INFINITY ? 1.f : exp2_fast(y.x - top);
+            sum = l * e0 + y.y * e1;
+            const float used = lu * e0 + y.w * e1;
+            mine = used == 0.f ? 0.f : e0 * v_mul / used;
+            theirs = used == 0.f ? 0.f : e1 * y.z / used;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              fm[k] = __shfl_sync(0xffffffffu, mine, 8 * k + fr);
+              ft[k] = __shfl_sync(0xffffffffu, theirs, 8 * k + fr);
+            }
+          }
+          if (any_rows) {
+#pragma unroll
+            for (int c = 0; c < C::COLS; c += 16)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                float o[8];
+                tmem_ld_frag16(tO + (hf << 20) + keep + c, o);
+                const float* at = box + (w * PIECES + c / 4 + hf * 2) * 512;
+                const float4 y0 = *reinterpret_cast<const float4*>(at), y1 = *reinterpret_cast<const float4*>(at + 512);
+                const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = o[e] * fm[2 * hf + ((e >> 1) & 1)] + y[e] * ft[2 * hf + ((e >> 1) & 1)];
+                store16(o, hf, keep + c);
+              }
+          }
+          // both go on when the boxes are read: they are filled again, or with the next segment's Q
+          mbar_arrive(half_empty);
           ok = mbar_wait<true>(half_empty, (uint32_t)hn & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
           if (!ok) break;
           ++hn;
@@ -764,6 +837,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       }
       tc_fence_before();
       tn += nt;
+      ++segment;
     }
   }
 
