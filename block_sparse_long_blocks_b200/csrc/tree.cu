@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the combining kernel may be scheduled; it waits for this one's results
   asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kWarps * 32) {  // (warp 0 has the axis to build)
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, kWarps);
@@ -800,6 +800,21 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
   const int lr = row & (a.rows - 1);
   // its partial in CTA c: the CTA's first segment, unless the unit begins inside the CTA's share
   auto part = [&](int c) { return (long long)(2 * c + ((long long)c * share < x0 ? 1 : 0)) * a.rows + lr; };
+  auto load_row = [&](int c, float* y) {
+    const float* src = a.part_o + part(c) * D + lane * PER;
+    if constexpr (PER == 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+      y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+    } else {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+      y[0] = x.x, y[1] = x.y;
+    }
+  };
+  // the rows of the first round come beside their weights
+  constexpr int ROUND = 32 / WARPS;
+  float ahead[ROUND][PER];
+#pragma unroll
+  for (int j = 0; j < ROUND; ++j) load_row(min(c0 + warp + j * WARPS, c1), ahead[j]);
   float w[MOST], big = -INFINITY;
 #pragma unroll
   for (int k = 0; k < MOST; ++k) {
@@ -824,18 +839,16 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
   for (int k = 0; k < MOST; ++k) {
     if (c0 + 32 * k > c1) break;
 #pragma unroll
-    for (int j = 0; j < 32 / WARPS; ++j) {  // (loads of one round are independent)
+    for (int j = 0; j < ROUND; ++j) {  // (loads of one round are independent)
       const int l = warp + j * WARPS, c = c0 + 32 * k + l;
       const float f = __shfl_sync(0xffffffffu, w[k], l);
       if (c > c1) continue;
-      const float* src = a.part_o + part(c) * D + lane * PER;
       float y[PER];
-      if constexpr (PER == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-        y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+      if (k == 0) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) y[e] = ahead[j][e];
       } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        y[0] = x.x, y[1] = x.y;
+        load_row(c, y);
       }
 #pragma unroll
       for (int e = 0; e < PER; ++e) v[e] += f == 0.f ? 0.f : f * y[e];

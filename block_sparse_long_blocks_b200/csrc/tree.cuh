@@ -157,14 +157,15 @@ __device__ __forceinline__ int group_of(const TreeArgs& a, int row) {
 }
 // x / y for 0 <= x, 0 < y: below 2^20 the float32 quotient (off by 2^-22 of it) is wrong by one at most.
 __device__ __forceinline__ int quotient(int x, int y) {
-  if (x >= 1 << 20 || y >= 1 << 20) return x / y;
+  if (x < y) return 0;
+  if (x >= 1 << 20) return x / y;
   int q = (int)__fdividef((float)x, (float)y);
   const int rest = x - q * y;
   return rest < 0 ? q - 1 : rest >= y ? q + 1 : q;
 }
 
 __device__ __forceinline__ int share_of(const TreeArgs& a, int total) {
-  return max((total + a.grid - 1) / a.grid, a.min_share);
+  return max(quotient(total + a.grid - 1, a.grid), a.min_share);
 }
 
 // One run of tiles of one unit within a CTA's share.
