@@ -52,7 +52,8 @@ template <bool E4M3>
 struct Roles {
   static constexpr int THREADS = E4M3 ? 512 : 384;
   static constexpr int CONVERT_WARP = E4M3 ? 12 : 11;
-  static constexpr int CONVERTERS = E4M3 ? 128 : 32;  // threads
+  static constexpr int GROUPS = E4M3 ? 2 : 1;         // of converters, which take the V tiles in turn
+  static constexpr int CONVERTERS = E4M3 ? 64 : 32;   // threads of a group
   // launched with 128 or 168 registers a thread: 2 x 128 x 176 + 256 x 80 = 512 x 128,
   // 2 x 128 x 200 + 128 x 104 = 384 x 168
   static constexpr uint32_t LAUNCH_REGS = E4M3 ? 128 : 168;
@@ -143,13 +144,14 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* warp_sum = reinterpret_cast<int*>(tmem_slot + 2);             // [16]
-  volatile uint32_t* s_vmax = tmem_slot + 18;                        // [kScales][4]
+  volatile uint32_t* s_vmax = tmem_slot + 18;                        // [kScales][2]
   volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 50);  // [kFlags][4]
   Axis axis(tmem_slot + 84, a.g.R);
 
   const CacheGeometry& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x < kFlags * 4) s_odd[threadIdx.x] = 0;
   if (TOKEN && threadIdx.x < kKeys) s_ones[threadIdx.x] = 1.f;
   if (threadIdx.x == (kMmaWarp + 1) * 32) {  // (warp 0 has the axis to build)
     constexpr uint32_t issuers = PAIR ? 2 : 1;  // that multiply with a tile
@@ -368,21 +370,15 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
     }
   } else if (warp >= L::CONVERT_WARP) {
     // ------------------------------------------------------------------ converters
-    const int ct = threadIdx.x - L::CONVERT_WARP * 32, cw = warp - L::CONVERT_WARP;
+    const int cw = warp - L::CONVERT_WARP, team = L::GROUPS == 1 ? 0 : cw >> 1;
+    const int ct = threadIdx.x - (L::CONVERT_WARP * 32 + team * L::CONVERTERS);
     int tn = 0, segment = 0;
     for (int x = x_begin; x < x_end && ok;) {
       Segment sg;
       if (!next_segment(a, axis, x, x_end, r, sg)) continue;
       const int nt = sg.t1 - sg.t0;
-      bool fresh = true;  // the segment's flag is not cleared yet
-      auto flag_odd = [&](bool odd) {
-        volatile int* f = s_odd + segment % kFlags * 4 + cw;
-        if (fresh && lane == 0) *f = 0;
-        fresh = false;
-        __syncwarp();
-        if (odd) *f = 1;
-      };
       for (int i = 0; i < nt; ++i, ++tn) {
+        if (L::GROUPS == 2 && (tn & 1) != team) continue;
         const int vs = tn % C::V_SLOTS, ms = tn % C::M_SLOTS;
         ok = mbar_wait<true>(v_full + vs, (uint32_t)(tn / C::V_SLOTS) & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
         if (!ok) break;
@@ -417,7 +413,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           const uint8_t* src = sV + vs * C::LOAD;
 #pragma unroll 4
           for (int q = ct; q < kKeys * 8; q += L::CONVERTERS) {
-            const int key = q >> 3, g8 = q & 7, sw = key & 7;
+            // eight threads take four granules each of keys k and k ^ 5: their 16-byte places differ in the swizzled
+            // row that is read and in the two that are written
+            const int key = ((q >> 6) << 3) | (((q >> 4) & 3) ^ ((q & 4) ? 5 : 0));
+            const int g8 = (q & 3) | ((q >> 1) & 4), sw = key & 7;
             uint4 w = *reinterpret_cast<const uint4*>(src + key * 128 + ((g8 ^ sw) << 4));
             if (special && pos0 + key >= sg.base) {
               const uint32_t m = 0x7f7f7f7fu;
@@ -435,24 +434,28 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
                 make_uint4(widen_lo(w.z), widen_hi(w.z), widen_lo(w.w), widen_hi(w.w));
           }
           if constexpr (TOKEN) {
-            float& at = s_vsc[tn % kScales * kKeys + ct];  // (a converter per key)
-            float sc = at;
+            float2& at = reinterpret_cast<float2*>(s_vsc + tn % kScales * kKeys)[ct];  // (two keys per converter)
+            float2 sc = at;
             if (special) {
-              const int pos = pos0 + ct;
-              if (pos >= sg.kv) {
-                sc = 0.f;
-              } else if (pos >= sg.base && !(sc < INFINITY)) {
-                sc = 0.f;
-                odd = true;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& y = e ? sc.y : sc.x;
+                const int pos = pos0 + 2 * ct + e;
+                if (pos >= sg.kv) {
+                  y = 0.f;
+                } else if (pos >= sg.base && !(y < INFINITY)) {
+                  y = 0.f;
+                  odd = true;
+                }
               }
               at = sc;
             }
             // (scales are not negative: they compare as integers)
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(sc));
-            if (lane == 0) s_vmax[tn % kScales * 4 + cw] = top;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(sc.x), __float_as_uint(sc.y)));
+            if (lane == 0) s_vmax[tn % kScales * 2 + (cw & 1)] = top;
           }
         }
-        if (special) flag_odd(odd);
+        if (odd) s_odd[segment % kFlags * 4 + cw] = segment + 1;
         // the tensor cores read the tile through the async proxy
         if (E4M3 || special) fence_async();
         mbar_arrive(m_full + ms);
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
                                FP_DEV_TIMEOUT);
           if (!ok) break;
           const int at = (tn + i) % kScales;
-          const uint32_t top = max(max(s_vmax[at * 4], s_vmax[at * 4 + 1]), max(s_vmax[at * 4 + 2], s_vmax[at * 4 + 3]));
+          const uint32_t top = max(s_vmax[at * 2], s_vmax[at * 2 + 1]);
           // the next power of two above it, within 2^-100 .. 2^127
           const uint32_t need = top == 0 ? 0 : min(max((top >> 23) + 1u, 27u), 254u);
           if (need > v_exp) {  // (all threads agree)
@@ -715,27 +718,39 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       // ---- the segment's rows
       const bool whole = sg.whole();
       const long long part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
-      auto odd_values = [](volatile int* f) { return E4M3 ? (f[0] | f[1] | f[2] | f[3]) != 0 : f[0] != 0; };
+      auto odd_values = [&](volatile int* f) {
+        const int s1 = segment + 1;
+        return E4M3 ? f[0] == s1 || f[1] == s1 || f[2] == s1 || f[3] == s1 : f[0] == s1;
+      };
       const bool odd = sg.t1 * kKeys > sg.base && odd_values(s_odd + segment % kFlags * 4);
-      const long long out = whole ? ((long long)(sg.off + tok) * a.Hq + sg.head * a.G + h) * D : (part * a.rows + lr) * D;
-      // This lane's fragment rows: lane / 4 + 8 k of the warp's.
+      // This lane's fragments: rows lane / 4 + 8 k of the warp's (k = 0 .. 3), columns 2 (lane % 4) + {0, 1} of eight.
+      // Where they go, in bytes. (A thread that stored its own row wrote 32 lines per store, which took 9000 clocks.)
       const int fr = lane >> 2, fc = 2 * (lane & 3);
-      // O's columns c0 .. c0 + 15 of 16 rows (half hf), as fragments with their rows' factors applied, go out. A thread
-      // that stored its own row wrote 32 lines per store, which took 9000 clocks.
-      auto store16 = [&](const float* f, int hf, int c0) {
+      uint8_t* to[4];
+      int row_tok[4];
+      {
+        uint8_t* mine = whole ? reinterpret_cast<uint8_t*>(a.o + ((long long)(sg.off + tok) * a.Hq + sg.head * a.G + h) * D)
+                              : reinterpret_cast<uint8_t*>(a.part_o + (part * a.rows + lr) * D);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned long long there = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), 8 * k + fr);
+          to[k] = 8 * k + fr < rows_in ? reinterpret_cast<uint8_t*>(there) : nullptr;
+          row_tok[k] = __shfl_sync(0xffffffffu, tok, 8 * k + fr);
+        }
+      }
+      // columns c0 .. c0 + 15 of 16 rows (half hf) with their rows' factors applied
+      auto store16 = [&](float* f, int hf, int c0) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int rr = hf * 16 + 8 * k + fr;
-          const long long to = __shfl_sync(0xffffffffu, out, rr) + c0 + fc;
-          const int t = odd ? __shfl_sync(0xffffffffu, tok, rr) : 0;
-          if (rr < rows_in) {
+          uint8_t* at = hf ? to[2 + k] : to[k];
+          if (at == nullptr) continue;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float2 v = make_float2(f[4 * j + 2 * k], f[4 * j + 2 * k + 1]);
-              if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, t, c0 + 8 * j + fc, kKeys, v);
-              if (whole) *reinterpret_cast<uint32_t*>(a.o + to + 8 * j) = pack2<false>(v.x, v.y);
-              else *reinterpret_cast<float2*>(a.part_o + to + 8 * j) = v;
-            }
+          for (int j = 0; j < 2; ++j) {
+            float2 v = make_float2(f[4 * j + 2 * k], f[4 * j + 2 * k + 1]);
+            const int d = c0 + 8 * j + fc;
+            if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, hf ? row_tok[2 + k] : row_tok[k], d, kKeys, v);
+            if (whole) *reinterpret_cast<uint32_t*>(at + 2 * d) = pack2<false>(v.x, v.y);
+            else *reinterpret_cast<float2*>(at + 4 * d) = v;
           }
         }
       };
