@@ -139,7 +139,7 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;
 // E4M3: cache type; TOKEN: token scales; NB: blocks of 8 rows held by every warp.
 template <bool E4M3, bool TOKEN, int D, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
   using C = Cfg<E4M3, D, NB>;
   constexpr int BLOCKS = C::TILE / kWarps / 16;         // 16-key blocks per warp and tile,
   constexpr int STEPS = NB == 4 || BLOCKS < 2 ? 1 : 2;  // of which so many share a softmax update
@@ -739,10 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d = round * C::RED_COLS + col;
         const int t = group_of(a, row), h = row - t * a.G;
         if (odd) {
-          float2 lo = make_float2(acc.x, acc.y), hi = make_float2(acc.z, acc.w);
-          add_odd_values<E4M3, TOKEN, D>(a, sg, t, d, C::TILE, lo);
-          add_odd_values<E4M3, TOKEN, D>(a, sg, t, d + 2, C::TILE, hi);
-          acc = make_float4(lo.x, lo.y, hi.x, hi.y);
+          const float2 lo = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0, min(sg.kv, sg.t1 << a.tile_shift), t, d);
+          const float2 hi = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0, min(sg.kv, sg.t1 << a.tile_shift), t, d + 2);
+          acc = make_float4(acc.x + lo.x, acc.y + lo.y, acc.z + hi.x, acc.w + hi.y);
         }
         if (whole) {
           *reinterpret_cast<uint2*>(a.o + ((long long)(sg.off + t) * a.Hq + sg.head * a.G + h) * D + d) =
@@ -760,111 +759,116 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // combining partial rows
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 
-// One CTA per (token, query head) row: the partial rows its unit left in the
-// workspace, in CTA order. Every warp holds all their weights (at most one
-// partial row per SM: a few registers a lane) and sums every eighth row, with
-// up to four loads in flight; a loop of dependent loads, weight before row, took 8-16 us.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
-  constexpr int WARPS = kMergeThreads / 32;
-  constexpr int MOST = 8;       // partial rows per lane: up to 256 SMs
+// The partial rows that a (token, query head) row's unit left in the workspace,
+// in CTA order. WIDE: a row per CTA, whose warps sum every eighth partial row
+// each; otherwise a row per warp. Which: a CTA has a prologue of a microsecond,
+// so many rows go to as many CTAs as run at once, warp by warp (64512 rows, most
+// of them finished before: 207 us with a CTA each, 56 us so), and few rows get
+// the latency of a CTA. Loads of four rows are in flight, the first ones beside
+// the rows' logarithms; a loop of dependent loads took 8-16 us.
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int SPLIT = WIDE ? kMergeWarps : 1;  // warps of a row
+  constexpr int MOST = 8;       // logarithms per lane: up to 256 SMs
   constexpr int PER = D / 32;   // columns per lane
+  constexpr int BATCH = 4;
   extern __shared__ int4 axis_mem[];
-  __shared__ int warp_sum[WARPS];
-  __shared__ float acc[WARPS][D];
+  __shared__ int warp_sum[kMergeWarps];
+  __shared__ float acc[WIDE ? kMergeWarps : 1][D];
   const CacheGeometry& g = a.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int token = blockIdx.x / a.Hq, hq = blockIdx.x - token * a.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = WIDE ? warp : 0;
   Axis axis(axis_mem, g.R);
   axis.build(a, warp_sum);
-  const int total = axis.total();
-  // the request of this token
-  int r = 0;
-  for (int hi = g.R - 1; r < hi;) {
-    const int mid = (r + hi) >> 1;
-    if (__ldg(g.cu + mid + 1) > token) hi = mid;
-    else r = mid + 1;
-  }
-  const Span sp = axis.span(a, r);
+  const int share = share_of(a, axis.total()), rows = g.total_tokens * a.Hq;
   // every thread waits, also those with nothing to do: this grid is not to end
   // before the one that it depends on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (sp.n == 0 || token < sp.off || token >= sp.off + sp.n) return;
-  const int nt = tiles_of(a, sp), head = hq / a.G, row = (token - sp.off) * a.G + hq - head * a.G;
-  const int x0 = axis.first(r) + (head * units_of(a, sp) + (row >> a.rows_shift)) * (a.lead + nt), x1 = x0 + a.lead + nt;
-  const int share = share_of(a, total);
-  const int c0 = (x0 + a.lead) / share, c1 = (x1 - 1) / share;
-  if (c0 == c1) return;  // one CTA had the whole unit and finished it
-  const int lr = row & (a.rows - 1);
-  // its partial in CTA c: the CTA's first segment, unless the unit begins inside the CTA's share
-  auto part = [&](int c) { return (long long)(2 * c + ((long long)c * share < x0 ? 1 : 0)) * a.rows + lr; };
-  auto load_row = [&](int c, float* y) {
-    const float* src = a.part_o + part(c) * D + lane * PER;
-    if constexpr (PER == 4) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-      y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
-    } else {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-      y[0] = x.x, y[1] = x.y;
+  const int step = gridDim.x * (WIDE ? 1 : kMergeWarps);
+  for (long long at = WIDE ? blockIdx.x : blockIdx.x * kMergeWarps + warp; at < rows; at += step) {
+    const int i = (int)at, token = quotient(i, a.Hq), hq = i - token * a.Hq;
+    // the request of this token
+    int r = 0;
+    for (int hi = g.R - 1; r < hi;) {
+      const int mid = (r + hi) >> 1;
+      if (__ldg(g.cu + mid + 1) > token) hi = mid;
+      else r = mid + 1;
     }
-  };
-  // the rows of the first round come beside their weights
-  constexpr int ROUND = 32 / WARPS;
-  float ahead[ROUND][PER];
-#pragma unroll
-  for (int j = 0; j < ROUND; ++j) load_row(min(c0 + warp + j * WARPS, c1), ahead[j]);
-  float w[MOST], big = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < MOST; ++k) {
-    const int c = c0 + lane + 32 * k;
-    w[k] = c <= c1 ? __ldcg(a.part_lse + part(c)) : -INFINITY;
-    big = fmaxf(big, w[k]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-  const float ref = big == -INFINITY ? 0.f : big;
-  float sum = 0.f, v[PER];
-#pragma unroll
-  for (int k = 0; k < MOST; ++k) {
-    w[k] = exp2_fast(w[k] - ref);
-    sum += w[k];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-  for (int e = 0; e < PER; ++e) v[e] = 0.f;
-#pragma unroll
-  for (int k = 0; k < MOST; ++k) {
-    if (c0 + 32 * k > c1) break;
-#pragma unroll
-    for (int j = 0; j < ROUND; ++j) {  // (loads of one round are independent)
-      const int l = warp + j * WARPS, c = c0 + 32 * k + l;
-      const float f = __shfl_sync(0xffffffffu, w[k], l);
-      if (c > c1) continue;
-      float y[PER];
-      if (k == 0) {
-#pragma unroll
-        for (int e = 0; e < PER; ++e) y[e] = ahead[j][e];
+    const Span sp = axis.span(a, r);
+    if (sp.n == 0 || token < sp.off || token >= sp.off + sp.n) continue;
+    const int head = group_of(a, hq), row = (token - sp.off) * a.G + hq - head * a.G, nt = tiles_of(a, sp);
+    const int x0 = axis.first(r) + (head * units_of(a, sp) + (row >> a.rows_shift)) * (a.lead + nt), x1 = x0 + a.lead + nt;
+    const int c0 = quotient(x0 + a.lead, share), c1 = quotient(x1 - 1, share);
+    if (c0 == c1) continue;  // one CTA had the whole unit and finished it
+    const int lr = row & (a.rows - 1);
+    // its partial in CTA c: the CTA's first segment, unless the unit begins inside the CTA's share
+    auto part = [&](int c) { return (long long)(2 * c + ((long long)c * share < x0 ? 1 : 0)) * a.rows + lr; };
+    auto load_row = [&](int c, float* y) {
+      const float* src = a.part_o + part(c) * D + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+        y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
       } else {
-        load_row(c, y);
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        y[0] = x.x, y[1] = x.y;
+      }
+    };
+    float y[BATCH][PER], w[MOST], big = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) load_row(min(c0 + first + j * SPLIT, c1), y[j]);
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      const int c = c0 + lane + 32 * k;
+      w[k] = c <= c1 ? __ldcg(a.part_lse + part(c)) : -INFINITY;
+      big = fmaxf(big, w[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    const float ref = big == -INFINITY ? 0.f : big;
+    float sum = 0.f, v[PER];
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) sum += exp2_fast(w[k] - ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) v[e] = 0.f;
+    for (int c = c0 + first; c <= c1; c += BATCH * SPLIT) {
+      if (c != c0 + first) {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) load_row(min(c + j * SPLIT, c1), y[j]);
       }
 #pragma unroll
-      for (int e = 0; e < PER; ++e) v[e] += f == 0.f ? 0.f : f * y[e];
+      for (int j = 0; j < BATCH; ++j) {
+        const int cj = c + j * SPLIT;
+        const float f = cj <= c1 ? exp2_fast(__ldcg(a.part_lse + part(cj)) - ref) : 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] += f == 0.f ? 0.f : f * y[j][e];
+      }
     }
-  }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat16* out = a.o + ((long long)token * a.Hq + hq) * D;
+    if constexpr (WIDE) {
 #pragma unroll
-  for (int e = 0; e < PER; ++e) acc[warp][lane * PER + e] = v[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float o = 0.f;
+      for (int e = 0; e < PER; ++e) acc[warp][lane * PER + e] = v[e];
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float o = 0.f;
 #pragma unroll
-    for (int k = 0; k < WARPS; ++k) o += acc[k][threadIdx.x];
-    a.o[((long long)token * a.Hq + hq) * D + threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+        for (int k = 0; k < kMergeWarps; ++k) o += acc[k][threadIdx.x];
+        out[threadIdx.x] = __float2bfloat16_rn(o * inv);
+      }
+      __syncthreads();
+    } else {
+      uint32_t p[PER / 2];
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) p[e] = pack2<false>(v[2 * e] * inv, v[2 * e + 1] * inv);
+      if constexpr (PER == 4) *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(p[0], p[1]);
+      else *reinterpret_cast<uint32_t*>(out + lane * 2) = p[0];
+    }
+    if (a.lse && lane == 0 && (!WIDE || warp == 0))
+      a.lse[(long long)hq * g.total_tokens + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
   }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(long long)hq * g.total_tokens + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------------------
@@ -907,8 +911,11 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
 
 template <int D>
 cudaError_t run_merge(const TreeArgs& a, cudaStream_t s) {
+  const long long rows = (long long)a.g.total_tokens * a.Hq, resident = (long long)a.grid * 8;
+  const bool wide = rows <= 2 * resident;
+  const long long ctas = wide ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)a.g.total_tokens * a.Hq));
+  cfg.gridDim = dim3((unsigned)(ctas < resident || wide ? ctas : resident));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = (size_t)axis_bytes(a.g.R);
   cfg.stream = s;
@@ -917,7 +924,8 @@ cudaError_t run_merge(const TreeArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, true>, a)
+              : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, false>, a);
 }
 
 template <bool E4M3, bool TOKEN, int D>

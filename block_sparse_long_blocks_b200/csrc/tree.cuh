@@ -265,25 +265,29 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Infinities and NaN that new tokens of this segment hold in two columns of V
-// reach the rows that see them (rare: they entered the products as zeros).
+// Infinities and NaN that new tokens of a segment (tiles t0 .., positions below
+// `end`) hold in two columns of V reach the rows that see them: their sums for
+// token t, else zeros (rare: they entered the products as zeros). By value, so
+// that nothing of the callers' has to lie in memory.
 template <bool E4M3, bool TOKEN, int D>
-__device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg, int t, int d, int tile, float2& acc) {
+__device__ __noinline__ float2 odd_values(const TreeArgs& a, int r, int off, int head, int base, int t0, int end, int t,
+                                          int d) {
+  float2 acc = make_float2(0.f, 0.f);
   const CacheGeometry& g = a.g;
-  const int32_t* row = g.table + (long long)sg.r * g.max_pages;
-  for (int pos = max(sg.base, sg.t0 * tile); pos < min(sg.kv, sg.t1 * tile); ++pos) {
-    const int j = pos - sg.base;
-    const bool see = a.mask ? (__ldg(a.mask + (long long)(sg.off + t) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u : j <= t;
+  const int32_t* row = g.table + (long long)r * g.max_pages;
+  for (int pos = max(base, t0 << a.tile_shift); pos < end; ++pos) {
+    const int j = pos - base;
+    const bool see = a.mask ? (__ldg(a.mask + (long long)(off + t) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u : j <= t;
     const int page = __ldg(row + (pos >> g.page_shift));
     if (!see || page < 0 || page >= g.num_pages) continue;
     const long long slot = ((long long)page << g.page_shift) + (pos & (g.page_size - 1));
-    const long long at = (slot * g.Hkv + sg.head) * D + d;
+    const long long at = (slot * g.Hkv + head) * D + d;
     float2 v;
     if constexpr (E4M3) {
       const uint32_t w = widen_lo(*reinterpret_cast<const uint16_t*>(g.v_pool + at));
       v = __half22float2(*reinterpret_cast<const __half2*>(&w));
       if (TOKEN) {
-        const float sc = __ldg(g.v_scale + (((long long)page * g.Hkv + sg.head) << g.page_shift) + (pos & (g.page_size - 1)));
+        const float sc = __ldg(g.v_scale + (((long long)page * g.Hkv + head) << g.page_shift) + (pos & (g.page_size - 1)));
         v.x *= sc;
         v.y *= sc;
       }
@@ -294,6 +298,7 @@ __device__ __noinline__ void add_odd_values(const TreeArgs& a, const Segment& sg
     if (!isfinite(v.x)) acc.x += v.x;
     if (!isfinite(v.y)) acc.y += v.y;
   }
+  return acc;
 }
 
 // Lets a kernel take all the dynamic shared memory a CTA can have: once per kernel and

@@ -112,7 +112,7 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 
 template <bool E4M3, bool TOKEN, int D, bool PAIR>
 __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+    wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
   using C = Cfg<E4M3, D, PAIR>;
   using L = Roles<E4M3>;
   extern __shared__ uint8_t smem_raw[];
@@ -718,11 +718,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       // ---- the segment's rows
       const bool whole = sg.whole();
       const long long part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
-      auto odd_values = [&](volatile int* f) {
+      auto flagged = [&](volatile int* f) {
         const int s1 = segment + 1;
         return E4M3 ? f[0] == s1 || f[1] == s1 || f[2] == s1 || f[3] == s1 : f[0] == s1;
       };
-      const bool odd = sg.t1 * kKeys > sg.base && odd_values(s_odd + segment % kFlags * 4);
+      const bool odd = sg.t1 * kKeys > sg.base && flagged(s_odd + segment % kFlags * 4);
       // This lane's fragments: rows lane / 4 + 8 k of the warp's (k = 0 .. 3), columns 2 (lane % 4) + {0, 1} of eight.
       // Where they go, in bytes. (A thread that stored its own row wrote 32 lines per store, which took 9000 clocks.)
       const int fr = lane >> 2, fc = 2 * (lane & 3);
@@ -748,7 +748,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           for (int j = 0; j < 2; ++j) {
             float2 v = make_float2(f[4 * j + 2 * k], f[4 * j + 2 * k + 1]);
             const int d = c0 + 8 * j + fc;
-            if (odd) add_odd_values<E4M3, TOKEN, D>(a, sg, hf ? row_tok[2 + k] : row_tok[k], d, kKeys, v);
+            if (odd) {
+              const float2 add = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0,
+                                                            min(sg.kv, sg.t1 * kKeys), hf ? row_tok[2 + k] : row_tok[k], d);
+              v = make_float2(v.x + add.x, v.y + add.y);
+            }
             if (whole) *reinterpret_cast<uint32_t*>(at + 2 * d) = pack2<false>(v.x, v.y);
             else *reinterpret_cast<float2*>(at + 4 * d) = v;
           }
