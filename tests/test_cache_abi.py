@@ -171,3 +171,25 @@ def test_reference_rows_that_see_nothing():
     c.see[:] = False
     O, lse, _, _ = pc.tree_attention(c.oracle(), c.cu.numpy(), c.q.double().numpy(), c.see, 1.0)
     assert (O == 0).all() and np.isneginf(lse).all()
+
+
+def test_native_calls_check_before_any_cuda_call(lib):
+    """The per-step calls refuse CPU tensors of the wrong kind by ValueError, other objects by TypeError."""
+    c = Case([5, 9], [1, 2], hkv=2, G=2, seed=3)
+    cache = fb.Cache(c.pool["k"], c.pool["v"], c.table, c.kv_lens)
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    for cu, a, b in ((c.cu.long(), k, k), (c.cu[:-1], k, k), (c.cu, k.float(), k), (c.cu, k, k[:2]), (c.cu, k[0], k[0]),
+                     (c.cu, k[:, :1], k[:, :1]), (c.cu, k.transpose(1, 2).contiguous().transpose(1, 2), k)):
+        with pytest.raises(ValueError):
+            fb.fp_cache_write(cache, cu, a, b)
+        with pytest.raises(ValueError):
+            fb.fp_cache_read(cache, cu, a, b)
+    with pytest.raises(ValueError):
+        fb.fp_cache_read(cache, c.cu, k, k, starts=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        fb.fp_cache_commit(cache, c.cu, 3, torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
+                           torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        fb.fp_cache_write(cache, [0, 1, 3], k, k)
+    with pytest.raises(TypeError):
+        fb.fp_cache_write(cache, c.cu, k, None)

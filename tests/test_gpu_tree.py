@@ -308,3 +308,82 @@ def test_a_decoding_run_over_a_prefilled_cache(fmt):
         fb.fp_tree_attention(plan, step, q, outs[-1])
     assert torch.equal(outs[0], outs[1])  # the same tiles of the same keys, whatever the pages
     assert fb.fp_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS + ["bf16_64"])
+@pytest.mark.parametrize("G,n", [(8, 1), (3, 5), (4, 9), (8, 16), (8, 17), (16, 40)])
+def test_every_kernel_over_keys_split_between_ctas(fmt, G, n):
+    """8, 16, 128 and 256 rows per unit, each over keys that many CTAs share, with short requests between long ones."""
+    c = Case([6000, 17 + n, 2500, n, 900], [n, 1, n, n, 0], hkv=2, G=G, page=32, fmt=fmt.replace("_64", ""),
+             d=64 if fmt.endswith("_64") else 128, seed=G + n)
+    run_and_check(c.trees())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("R", [33, 1030])
+@pytest.mark.parametrize("G", [4, 8, 16])
+def test_many_requests(fmt, R, G):
+    """More requests than a warp has lanes, and than the spans that shared memory holds; few and many rows."""
+    rng = np.random.default_rng(R + G)
+    n = rng.integers(0, 4, R)
+    kv = n + rng.integers(0, 90, R)
+    kv[R // 2], n[R // 2] = 2000, 3
+    run_and_check(Case(kv.tolist(), n.tolist(), hkv=1, G=G, fmt=fmt, seed=R).trees())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_combined_by_warps(fmt):
+    """More (token, head) rows than get a CTA each in the combining kernel, of split and of whole units."""
+    c = Case([3000] + [70] * 9, [64] * 10, hkv=4, G=1, page=64, fmt=fmt, seed=4)
+    assert c.total * c.hq > 2 * 148 * 8
+    run_and_check(c.trees())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("G,n", [(2, 3), (2, 7), (4, 9), (8, 20)])
+def test_unseen_values_in_every_kernel(fmt, G, n):
+    """NaN in V (and its scale) of a new token: rows that see it become NaN, others do not notice."""
+    kv = [n + 40, n + 131]
+    c = Case(kv, [n, n], hkv=2, G=G, fmt=fmt, seed=n).trees()
+    clean, clean_lse = c.cuda().attend()
+    at = torch.cat([c.new_slots(r)[[1]] for r in range(c.R)])
+    c.fill("v", at, float("nan"), scale=float("nan") if fmt == "e4m3_token" else None)
+    o, lse = c.cuda().attend()
+    sees = torch.from_numpy(np.concatenate([c.see[int(c.cu[r]):int(c.cu[r + 1]), 1] for r in range(c.R)])).cuda()
+    assert sees.any() and (~sees).any()
+    assert torch.isnan(o[sees].float()).all() and torch.isfinite(o[~sees].float()).all()
+    assert (o[~sees].float() - clean[~sees].float()).abs().max() <= 2.0 ** -7 * clean.float().abs().max()
+    assert torch.equal(lse, clean_lse) and fb.fp_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [3, 12, 40])
+def test_infinite_and_huge_queries(fmt, n):
+    """A query row of infinities gives NaN and leaves the others; one outlier element dominates a row."""
+    c = Case([90 + n], [n], hkv=1, G=4, fmt=fmt, seed=n)
+    clean, _ = c.cuda().attend()
+    c.q[1, 2] = float("inf")
+    c.q[0, 1, 7] = 300.0
+    o, lse = c.cuda().attend()
+    rest = torch.ones(c.total, c.hq, dtype=torch.bool, device="cuda")
+    rest[1, 2] = rest[0, 1] = False
+    assert torch.isnan(o[1, 2].float()).all() and torch.equal(o[rest], clean[rest])
+    assert torch.isfinite(o[0, 1].float()).all() and fb.fp_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt,n", [("bf16", 16), ("bf16", 64), ("e4m3_token", 16), ("e4m3_head", 64)])
+def test_waits_that_run_out_with_many_rows(fmt, n):
+    """As above for the kernels of 128 and 256 rows."""
+    short = fb.load_library(build.build_variant("short_wait"))
+    c = Case([60000], [n], hkv=4, G=4, page=64, fmt=fmt).trees().cuda()
+    o, lse = c.attend()
+    plan, out = c.plan(), torch.empty_like(o)
+    p = plan.p
+    p.cu_tokens, p.mask, p.mask_words = c.gpu["cu"].data_ptr(), c.gpu["mask"].data_ptr(), c.gpu["mask"].shape[1]
+    s = torch.cuda.current_stream().cuda_stream
+    assert short.fp_tree_attention(c.cache.ref, plan.ref, c.gpu["q"].data_ptr(), out.data_ptr(), None,
+                                   plan.workspace.data_ptr(), plan.ws_bytes, s) == 0
+    bits = ctypes.c_uint32(0)
+    assert short.fp_get_device_status(ctypes.byref(bits), s) == -6 and bits.value == fb.DEV_TIMEOUT
+    o2, lse2 = c.attend()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and fb.fp_get_device_status() == 0
