@@ -885,8 +885,16 @@ int sm_count() {
   return n;
 }
 
-// Rows per unit: the kernel here holds 8 or 16, the one for many rows (tree_wide.cu) one or two M-tiles of 128.
-int unit_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 128 ? 128 : 256; }
+// Rows per unit: the kernel here holds 8 or 16, the one for many rows (tree_wide.cu) one or two M-tiles of 128. 17 to
+// 32 rows are two units here where the page table has room for 1 MB of K and V per KV head at most: a segment of many
+// rows takes 25000 clocks beside its tiles, here 4500 (16 requests, 4 KV heads, 32 rows: 256 keys 15.1 -> 11.2 us,
+// 1024 keys 25.2 -> 21.9 us bf16 and 27.1 -> 15.4 us e4m3; 4096 keys 38.5 -> 43.8 us bf16, 40.9 -> 38.0 us e4m3).
+int unit_rows(const CacheGeometry& g, int max_rows) {
+  if (max_rows <= 8) return 8;
+  const long long bytes = (long long)g.max_pages * g.page_size * g.d * (g.e4m3 ? 2 : 4);
+  if (max_rows <= 16 || (max_rows <= 32 && bytes <= 1 << 20)) return 16;
+  return max_rows <= 128 ? 128 : 256;
+}
 
 // What a segment takes beside its tiles, in tiles.
 constexpr int kNarrowLead = 2, kWideLead = 6;
@@ -912,7 +920,14 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
 template <int D>
 cudaError_t run_merge(const TreeArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.g.total_tokens * a.Hq, resident = (long long)a.grid * 8;
-  const bool wide = rows <= 2 * resident;
+  // Rounds of CTAs, times a prologue and the loads of the partial rows that a row may have (four in flight per warp):
+  // about 1.5 us and 0.2 us a partial row of a warp. 512 rows of 37 parts: 60 us with a CTA each, 73 us with a warp;
+  // 2048 rows of 2 or 3: 32 us and 26 us.
+  const long long units = (long long)a.g.R * a.g.Hkv * ((a.max_tokens * a.G + a.rows - 1) / a.rows);
+  const double parts = units < a.grid ? (double)a.grid / units + 1 : 2;
+  const double by_cta = (double)((rows + resident - 1) / resident) * (1.5 + 0.2 * parts / kMergeWarps);
+  const double by_warp = (double)((rows + resident * kMergeWarps - 1) / (resident * kMergeWarps)) * (1.5 + 0.2 * parts);
+  const bool wide = by_cta <= by_warp;
   const long long ctas = wide ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ctas < resident || wide ? ctas : resident));
@@ -939,7 +954,7 @@ size_t pad256(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Two partial units per CTA: float32 O rows, then their logarithms.
 size_t tree_workspace(const CacheGeometry& g, int hq, int max_tokens) {
-  const size_t rows = (size_t)2 * sm_count() * unit_rows(max_tokens * (hq / g.Hkv));
+  const size_t rows = (size_t)2 * sm_count() * unit_rows(g, max_tokens * (hq / g.Hkv));
   return pad256(rows * g.d * sizeof(float)) + pad256(rows * sizeof(float));
 }
 
@@ -950,7 +965,7 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   a.Hq = t.hq;
   a.G = t.hq / g.Hkv;
   a.max_tokens = t.max_tokens;
-  a.rows = unit_rows(t.max_tokens * a.G);
+  a.rows = unit_rows(g, t.max_tokens * a.G);
   a.mask = t.mask;
   a.mask_words = t.mask_words;
   a.q = static_cast<const __nv_bfloat16*>(q);
