@@ -85,6 +85,8 @@ fp_status_t validate_tree(const fp_cache_t* c, const fp_tree_t* t) {
   const int G = t->hq / c->hkv;
   if (!(G <= 8 || G == 16) || t->max_tokens > kMaxNewTokens) return FP_ERR_UNSUPPORTED;
   if ((long long)t->total_tokens * t->hq > INT_MAX) return FP_ERR_UNSUPPORTED;
+  // positions are rounded up to whole tiles in an int
+  if ((long long)c->max_pages_per_req * c->page_size > INT_MAX - 1024) return FP_ERR_UNSUPPORTED;
   // the axis of all tiles (and up to 8 places before a unit's) is counted in an int
   const long long tiles = ((long long)c->max_pages_per_req * c->page_size + 127) / 128 + 8;
   const long long units = ((long long)t->max_tokens * G + 15) / 16 * c->hkv * c->batch;

@@ -253,7 +253,7 @@ size_t fp_static_scratch_bytes(void);
  *   that fp_prefill and fp_paged_sparse_prefill read, the scales given by the
  *   caller), or FP_SCALE_TOKEN, one per token and KV head (k_scale, v_scale:
  *   [num_pages, hkv, page_size]; written by fp_cache_write). The value of an
- *   e4m3 code is code * scale.
+ *   e4m3 code is code * scale. Scales are not negative.
  * - head_dim 128, or 64 with FP_BF16; page_size a power of two in 16..65536.
  *   Pools and scales are 16-byte aligned.
  * - "New tokens": cu_tokens (device int32 [batch + 1], non-decreasing,
@@ -362,6 +362,8 @@ size_t fp_tree_workspace_size(const fp_cache_t* c, const fp_tree_t* t);
  * The keys of all requests are divided evenly over the SMs; partial results
  * are combined in a fixed order, so equal calls give equal bits.
  * A request with n_r > max_tokens sets FP_DEV_BAD_SEQLENS and is skipped.
+ * o and lse overlap neither q nor the cache. Positions stay below 2^31 - 1024
+ * (max_pages_per_req * page_size, else FP_ERR_UNSUPPORTED).
  * workspace: fp_tree_workspace_size bytes, 256-byte aligned, contents
  * overwritten; calls that may overlap on the GPU need one each.
  */

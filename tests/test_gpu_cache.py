@@ -284,3 +284,57 @@ def test_offsets_past_32_bits():
     fb.fp_cache_commit(cache, cu, 300, torch.tensor([[5, 299]], dtype=torch.int32, device="cuda"),
                        torch.tensor([2], dtype=torch.int32, device="cuda"), lens)
     assert lens.item() == 702 and torch.equal(ks[-1, 0, 701], ks[-1, 0, 999]) and fb.fp_get_device_status() == 0
+
+
+@pytest.mark.parametrize("seed", [0, 1])
+def test_quotients_are_ieee_division(seed):
+    """Four million random bf16 values of every exponent, by scales with full mantissas (and some out of the
+    correction's range): the codes are those of float32 division."""
+    c = Case([2048, 2100], [2048, 2048], hkv=8, G=1, page=128, fmt="e4m3_head", seed=seed, poison=False)
+    g = torch.Generator().manual_seed(seed)
+    lo, hi = ((-10, 6), (-126, 126))[seed]
+    c.scale = {n: torch.exp2(torch.rand(8, generator=g) * (hi - lo) + lo) for n in "kv"}
+    rows = []
+    for n in "kv":
+        x = torch.randn(c.total, 8, 128, generator=g).double()
+        # values whose quotients spread over e4m3's range and beyond, many next to its rounding borders
+        x = x * c.scale[n][:, None].double() * torch.exp2(torch.randint(-12, 12, x.shape, generator=g).double())
+        rows.append(x.clamp(-3e38, 3e38).bfloat16())
+    want = written(c, rows)
+    c.cuda()
+    fb.fp_cache_write(c.cache, c.gpu["cu"], *(x.cuda() for x in rows))
+    check_cache(c, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_requests(fmt):
+    """More requests than one search step separates, many of them empty: write, read back, keep the first ones."""
+    rng = np.random.default_rng(3)
+    n = rng.integers(0, 4, 1030)
+    c = Case((n + rng.integers(0, 40, 1030)).tolist(), n.tolist(), hkv=2, G=1, fmt=fmt, seed=3)
+    rows = packed_rows(c)
+    want = written(c, rows)
+    c.cuda()
+    fb.fp_cache_write(c.cache, c.gpu["cu"], *(x.cuda() for x in rows))
+    check_cache(c, want)
+    out = [torch.full((c.total, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    fb.fp_cache_read(c.cache, c.gpu["cu"], *out)
+    for name, x in zip("kv", out):
+        at = torch.cat([c.new_slots(r) for r in range(c.R)])
+        vals = want[0][name].float().flatten(0, 1)[at]
+        if fmt == "e4m3_head":
+            vals = vals * c.scale[name][:, None]
+        elif fmt == "e4m3_token":
+            vals = vals * want[1][name][at // c.page, :, at % c.page][..., None]
+        assert same(x, vals.bfloat16())
+    num = torch.from_numpy((n > 1).astype(np.int32)).cuda()
+    new = torch.empty(c.R, dtype=torch.int32, device="cuda")
+    fb.fp_cache_commit(c.cache, c.gpu["cu"], c.total, torch.ones(c.R, 1, dtype=torch.int32, device="cuda"), num, new)
+    assert torch.equal(new.cpu(), c.kv_lens - torch.from_numpy(n).int() + num.cpu())
+    first = torch.from_numpy(np.concatenate([c.flat(r, [c.kv[r] - c.n[r]]).numpy() for r in range(c.R) if n[r] > 1]))
+    second = torch.from_numpy(np.concatenate([c.flat(r, [c.kv[r] - c.n[r] + 1]).numpy() for r in range(c.R) if n[r] > 1]))
+    for name in "kv":
+        want[0][name].view(torch.uint8).flatten(0, 1)[first] = want[0][name].view(torch.uint8).flatten(0, 1)[second]
+        if want[1][name] is not None and fmt == "e4m3_token":
+            want[1][name][first // c.page, :, first % c.page] = want[1][name][second // c.page, :, second % c.page]
+    check_cache(c, want)
