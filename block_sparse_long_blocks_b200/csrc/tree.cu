@@ -62,8 +62,8 @@ constexpr int kWarps = 8;                      // consumer warps
 constexpr int kThreads = (kWarps + 4) * 32;    // + the producer, alone in a third warpgroup
 // Registers: launched with 168 a thread (three warps per SM sub-partition); the consumers then
 // take 208 and the producer's warpgroup 88: 2 x 128 x 208 + 128 x 88 = 384 x 168.
-constexpr uint32_t kConsumerRegs = 208, kProducerRegs = 88;
-static_assert(2 * 128 * kConsumerRegs + 128 * kProducerRegs <= kThreads * 168, "register split exceeds the launch");
+constexpr uint32_t kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
+static_assert(2 * 128 * kConsumerRegs + 128 * kProducerRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kConsumers = kWarps * 32;
 constexpr int kTileBytes = 32 * 1024;          // of K, and of V
 
@@ -139,7 +139,8 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;
 // E4M3: cache type; TOKEN: token scales; NB: blocks of 8 rows held by every warp.
 template <bool E4M3, bool TOKEN, int D, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
+    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ TreeArgs a) {
   using C = Cfg<E4M3, D, NB>;
   constexpr int BLOCKS = C::TILE / kWarps / 16;         // 16-key blocks per warp and tile,
   constexpr int STEPS = NB == 4 || BLOCKS < 2 ? 1 : 2;  // of which so many share a softmax update
@@ -566,8 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 2; ++e) {
                 float& y = e ? vf.y : vf.x;
                 const int pos = pos0 + key + e;
-                if (pos >= sg.base && !(y < INFINITY)) {
-                  odd |= pos < sg.kv;
+                if (pos >= sg.kv) {
+                  y = 0.f;  // (whatever the slot held before: times a weight of zero it may be NaN)
+                } else if (pos >= sg.base && !(y < INFINITY)) {
+                  odd = true;
                   y = 0.f;
                 }
               }
@@ -679,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) s_odd[(segment + 1) & 1] = 0;  // (its readers have passed the barrier above)
     const bool whole = sg.whole();
     const int part = 2 * blockIdx.x + (segment == 0 ? 0 : 1);
+    float top[NB], all[NB];  // reference and sum of the rows over the warps
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const float* pm = s_m + gr + 8 * b;
@@ -691,7 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < kWarps; ++k)
         sum += pl2[k * C::ROWS] * (big == -INFINITY ? 1.f : exp2_fast(pm[k * C::ROWS] - big));
       float w = big == -INFINITY ? 1.f : exp2_fast(ref[b] - big);
-      w = sum == 0.f ? 0.f : w * v_mul / sum;
+      w = sum == 0.f ? 0.f : __fdividef(w * v_mul, sum);
+      top[b] = big;
+      all[b] = sum;
       const float w0 = __shfl_sync(0xffffffffu, w, 8 * c), w1 = __shfl_sync(0xffffffffu, w, 8 * c + 4);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -700,16 +706,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float we = (e & 1) ? w1 : w0;
           o[i][b][e] = we == 0.f ? 0.f : o[i][b][e] * we;
         }
-      if (warp == 0 && c == 0 && in[b]) {
-        // the weights' factor (e4m3) comes off the logarithm
-        const float lse2 = sum == 0.f ? -INFINITY : (big == -INFINITY ? 0.f : big) + log2f(sum) - (E4M3 ? kShift : 0.f);
-        if (!whole) {
-          a.part_lse[(long long)part * a.rows + gr + 8 * b] = lse2;
-        } else if (a.lse) {
-          const int h = sg.row0 + gr + 8 * b - tok[b] * a.G;
-          a.lse[(long long)(sg.head * a.G + h) * g.total_tokens + sg.off + tok[b]] = lse2 * 0.69314718055994531f;
-        }
-      }
     }
     const bool odd = s_odd[segment & 1] != 0;
 #pragma unroll
@@ -739,8 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d = round * C::RED_COLS + col;
         const int t = group_of(a, row), h = row - t * a.G;
         if (odd) {
-          const float2 lo = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0, min(sg.kv, sg.t1 << a.tile_shift), t, d);
-          const float2 hi = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0, min(sg.kv, sg.t1 << a.tile_shift), t, d + 2);
+          const int end = min(sg.kv, sg.t1 << a.tile_shift);
+          const float2 lo = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0, end, t, d);
+          const float2 hi = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0, end, t, d + 2);
           acc = make_float4(acc.x + lo.x, acc.y + lo.y, acc.z + hi.x, acc.w + hi.y);
         }
         if (whole) {
@@ -751,6 +748,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       consumers_sync();  // the next round, or the next segment's Q, may be written
+    }
+    if (warp == kWarps - 1 && c == 0) {  // (behind the barriers: the others are off to the next segment)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (!in[b]) continue;
+        // the weights' factor (e4m3) comes off the logarithm
+        const float lse2 =
+            all[b] == 0.f ? -INFINITY : (top[b] == -INFINITY ? 0.f : top[b]) + log2f(all[b]) - (E4M3 ? kShift : 0.f);
+        if (!whole) {
+          a.part_lse[(long long)part * a.rows + gr + 8 * b] = lse2;
+        } else if (a.lse) {
+          const int h = sg.row0 + gr + 8 * b - tok[b] * a.G;
+          a.lse[(long long)(sg.head * a.G + h) * g.total_tokens + sg.off + tok[b]] = lse2 * 0.69314718055994531f;
+        }
+      }
     }
     ++segment;
   }
@@ -910,8 +922,8 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
   using C = Cfg<E4M3, D, NB>;
   auto kern = tree_kernel<E4M3, TOKEN, D, NB>;
   const int smem = C::SMEM_FIXED + axis_bytes(a.g.R);
-  static std::atomic<unsigned long long> allowed{0};
-  const cudaError_t e = allow_shared(kern, allowed);
+  static std::atomic<unsigned long long> prepared{0};
+  const cudaError_t e = prepare(kern, kLaunchRegs, prepared);
   if (e != cudaSuccess) return e;
   kern<<<a.grid, kThreads, smem, s>>>(mk, mv, a);
   return cudaGetLastError();

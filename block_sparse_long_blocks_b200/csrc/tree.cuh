@@ -301,15 +301,19 @@ __device__ __noinline__ float2 odd_values(const TreeArgs& a, int r, int off, int
   return acc;
 }
 
-// Lets a kernel take all the dynamic shared memory a CTA can have: once per kernel and
-// device, as the runtime call costs a fifth of a launch.
+// Lets a kernel take all the dynamic shared memory a CTA can have, and checks that it was built with the registers
+// per thread that its setmaxnreg split counts on (a larger split would wait for registers for ever): once per kernel
+// and device, as the runtime calls cost a fifth of a launch.
 template <class K>
-cudaError_t allow_shared(K kern, std::atomic<unsigned long long>& done) {
+cudaError_t prepare(K kern, int launch_regs, std::atomic<unsigned long long>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  cudaFuncAttributes f;
+  if ((e = cudaFuncGetAttributes(&f, kern)) != cudaSuccess) return e;
+  if (f.numRegs < launch_regs) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;

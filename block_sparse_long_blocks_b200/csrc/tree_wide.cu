@@ -27,9 +27,10 @@
 // tokens or end behind the last one safe to multiply: rows behind the last token
 // become zeros, and so do infinities and NaN of new tokens, which only some rows
 // see (those are added to the rows that see them at the end).
-// An issuer may watch the phase of a slot only if it has seen all earlier ones
-// of that slot: key tiles alternate between the warpgroups over all segments,
-// and the K ring has an even number of slots, so a slot is always of one issuer.
+// An issuer may watch the phase of a slot only if all earlier ones of that slot
+// are over: key tiles alternate between the warpgroups over all segments, and
+// the K ring has an even number of slots, so a slot is always of one issuer;
+// V tiles come from the converters, in order where three slots are shared.
 // Every wait is bounded; after one ran out every role leaves its loop, the MMA
 // issuers and the producer wait for what they have in flight, outputs are
 // invalid and FP_DEV_TIMEOUT is set.
@@ -112,7 +113,8 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 
 template <bool E4M3, bool TOKEN, int D, bool PAIR>
 __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeArgs a) {
+    wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ TreeArgs a) {
   using C = Cfg<E4M3, D, PAIR>;
   using L = Roles<E4M3>;
   extern __shared__ uint8_t smem_raw[];
@@ -475,7 +477,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       Segment sg;
       if (!next_segment(a, axis, x, x_end, r, sg)) continue;
       const int nt = sg.t1 - sg.t0;
-      const int lr = PAIR ? w * 128 + row : row, rho = sg.row0 + lr;
+      // The unit's rows go round the warps, 4 i + warp in lane i: the start and the end of a segment, which take a warp
+      // as long as it has rows, are shared evenly by the four of a warpgroup also where rows are few.
+      const int lr = (PAIR ? w * 128 : 0) + 4 * lane + (warp & 3), rho = sg.row0 + lr;
       const bool in = rho < sg.n * a.G;
       const int tok = in ? group_of(a, rho) : 0, h = in ? rho - tok * a.G : 0;
       const int rows_in = __popc(__ballot_sync(0xffffffffu, in));  // (the warp's first ones)
@@ -803,6 +807,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             for (int c = 0; c < C::COLS; c += 16)
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
+                if (hf * 16 >= rows_in) continue;
                 float o[8];
                 tmem_ld_frag16(tO + (hf << 20) + give + c, o);
                 tmem_wait_ld();
@@ -834,6 +839,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             for (int c = 0; c < C::COLS; c += 16)
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
+                if (hf * 16 >= rows_in) continue;
                 float o[8];
                 tmem_ld_frag16(tO + (hf << 20) + keep + c, o);
                 const float* at = box + (w * PIECES + c / 4 + hf * 2) * 512;
@@ -873,8 +879,8 @@ cudaError_t run(const TreeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
   // more than half of the SM's shared memory: one CTA per SM, so that the
   // 512-column TMEM allocation never waits for a co-resident CTA
   const int want = C::SMEM_FIXED + axis_bytes(a.g.R), smem = want > 120 * 1024 ? want : 120 * 1024;
-  static std::atomic<unsigned long long> allowed{0};
-  const cudaError_t e = allow_shared(kern, allowed);
+  static std::atomic<unsigned long long> prepared{0};
+  const cudaError_t e = prepare(kern, (int)Roles<E4M3>::LAUNCH_REGS, prepared);
   if (e != cudaSuccess) return e;
   kern<<<a.grid, Roles<E4M3>::THREADS, smem, s>>>(mk, mv, a);
   return cudaGetLastError();

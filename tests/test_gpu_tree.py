@@ -387,3 +387,22 @@ def test_waits_that_run_out_with_many_rows(fmt, n):
     assert short.fp_get_device_status(ctypes.byref(bits), s) == -6 and bits.value == fb.DEV_TIMEOUT
     o2, lse2 = c.attend()
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and fb.fp_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", [1, 3, 9, 40])
+def test_what_an_earlier_call_left_in_shared_memory(fmt, n):
+    """The ring's slots hold another cache's keys, values and scales, as large as they get, behind a short request's last
+    token."""
+    big = Case([90000], [n], hkv=8, G=4, page=64, fmt=fmt, seed=1)
+    for name in "kv":
+        if fmt == "bf16":
+            big.pool[name].fill_(3e38)
+        else:
+            big.scale[name] = torch.full_like(big.scale[name], 3e38)
+    big.cuda().attend()
+    c = Case([17 + n, n, 300], [n, n, n], hkv=8, G=4, page=16, fmt=fmt, seed=2).trees().cuda()
+    for _ in range(3):
+        big.attend()
+        o, lse = c.attend()
+        check_tree(c, o, lse)
