@@ -265,6 +265,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// The whole producer warp, before a tile's copies: zeros for the scales of a bad page (its codes are zeros; whatever
+// scale another page has may be NaN). Returns the bytes that the scales' copies bring.
+__device__ __forceinline__ uint32_t scales_of_tile(float* scales, bool bad, bool mine, int lane, int sub_rows) {
+  if (__any_sync(0xffffffffu, bad)) {
+    if (bad)
+      for (int k = 0; k < sub_rows; ++k) scales[lane * sub_rows + k] = 0.f;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (later copies come to the same place)
+    __syncwarp();
+  }
+  return (uint32_t)__popc(__ballot_sync(0xffffffffu, mine && !bad)) * (uint32_t)sub_rows * 4u;
+}
+
 // Infinities and NaN that new tokens of a segment (tiles t0 .., positions below
 // `end`) hold in two columns of V reach the rows that see them: their sums for
 // token t, else zeros (rare: they entered the products as zeros). By value, so

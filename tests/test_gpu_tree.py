@@ -406,3 +406,33 @@ def test_what_an_earlier_call_left_in_shared_memory(fmt, n):
         big.attend()
         o, lse = c.attend()
         check_tree(c, o, lse)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("G,n", [(4, 1), (4, 3), (4, 9), (8, 20)])
+def test_a_bad_page_reads_as_zeros_whatever_other_pages_hold(fmt, G, n):
+    """Equal bits with a table that names a page of zeros instead, page 0 and its scales being NaN."""
+    outs = []
+    for bad in (False, True):
+        c = Case([330, 60], [n, 1], hkv=2, G=G, page=32, fmt=fmt, seed=6, extra_pages=4).trees()
+        used = set(c.table[0, :11].tolist()) | set(c.table[1, :2].tolist())
+        zeros = next(p for p in range(1, 17) if p not in used)
+        if 0 in used:  # page 0 changes places with a free one
+            other = next(p for p in range(zeros + 1, 17) if p not in used)
+            c.table[c.table == 0] = other
+            for name in "kv":
+                bits = c.pool[name].view(torch.uint8)
+                bits[other] = bits[0]
+                if fmt == "e4m3_token":
+                    c.scale[name][other] = c.scale[name][0]
+        for name in "kv":
+            c.pool[name].view(torch.uint8)[0] = 0xFF  # NaN
+            c.pool[name].view(torch.uint8)[zeros] = 0
+            if fmt == "e4m3_token":
+                c.scale[name][0] = float("nan")
+                c.scale[name][zeros] = 0
+        c.table[0, 4] = -3 if bad else zeros
+        outs.append(c.cuda().attend())
+        assert fb.fp_get_device_status() == (fb.DEV_BAD_PAGE if bad else 0)
+    assert torch.isfinite(outs[0][0].float()).all()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
