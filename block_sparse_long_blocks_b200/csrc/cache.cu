@@ -30,7 +30,7 @@ constexpr int kMoveThreads = 256;
 // whole prompts, e4m3: 220 us with 8 CTAs of one vector, 242 us with 5 of two); reading takes more loads each
 // (213 us with 5 of four, 294 us with 8, whose registers spill).
 constexpr int kWriteCtas = 8, kWriteVecs = 1, kReadCtas = 5, kReadVecs = 4;
-constexpr int kMaxTokensPerCta = 16;  // (64: reads of whole prompts at 213 us, not 197)
+constexpr int kMaxTokensPerCta = 64;
 enum Format { kBf16 = 0, kHeadScale = 1, kTokenScale = 2 };
 
 constexpr int kVec = 8;  // elements per thread and step
@@ -176,19 +176,34 @@ __device__ __forceinline__ float over_448(float m) {
   return m >= 0x1p-90f && m < INFINITY ? fmaf(fmaf(-q, 448.f, m), inv, q) : __fdiv_rn(m, 448.f);
 }
 
-// max |x| over the sixteen lanes that hold one head's 128 elements (NaN does not count)
-__device__ __forceinline__ float head_absmax(const uint4& in) {
-  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-  float m = 0.f;
+// max |x| of K's and of V's vector over the sixteen lanes that hold one head's 128 elements (NaN does not count). The
+// bits of |x| order as integers, so two values are compared at a time, and K and V share the shuffles.
+__device__ __forceinline__ float2 head_absmax(const uint4& k, const uint4& v) {
+  auto top = [](const uint4& x) {
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
+  };
+  const uint32_t tk = top(k), tv = top(v);
+  uint32_t both = __vmaxu2(__byte_perm(tk, tv, 0x5410), __byte_perm(tk, tv, 0x7632));  // low half K, high half V
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    unpack_bf16(w[i], a, b);
-    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+  for (int o = 8; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o, 16));
+  float2 out = make_float2(__uint_as_float(both << 16), __uint_as_float(both & 0xffff0000u));
+  // NaN bits are above infinity's: then the ordinary way
+  if (__any_sync(0xffffffffu, (both & 0xffffu) > 0x7f80u || (both >> 16) > 0x7f80u)) {
+    auto slow = [](const uint4& x) {
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float m = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack_bf16(w[i], a, b);
+        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+      }
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o, 16));
+      return m;
+    };
+    out = make_float2(slow(k), slow(v));
   }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o, 16));
-  return m;
+  return out;
 }
 
 struct MoveArgs {
@@ -237,6 +252,8 @@ __global__ void __launch_bounds__(kMoveThreads, kWriteCtas) cache_write_kernel(c
       if (__all_sync(0xffffffffu, i >= items)) continue;
       const int j = min(i, items - 1), t = __umulhi(j, a.vecs_inv), x = j - t * a.vecs;
       const long long s = i < items ? slot[t] : kSkip;
+      float2 top;
+      if constexpr (FMT == kTokenScale) top = head_absmax(in[0][u], in[1][u]);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         uint8_t* pool = which ? g.v_pool : g.k_pool;
@@ -247,7 +264,7 @@ __global__ void __launch_bounds__(kMoveThreads, kWriteCtas) cache_write_kernel(c
           const int head = x >> 4;
           float sc;
           if constexpr (FMT == kTokenScale) {
-            sc = over_448(head_absmax(in[which][u]));
+            sc = over_448(which ? top.y : top.x);
             if (s >= 0 && (x & 15) == 0) scales[scale_index(g, s, head)] = sc;
           } else {
             sc = __ldg(scales + head);
@@ -413,8 +430,11 @@ __global__ void __launch_bounds__(kMoveThreads)
   if (threadIdx.x == 0) new_lens[r] = base + num;
 }
 
-// Tokens per CTA: as few as fill the SMs' CTAs at most once, and up to the slots' array, so that one token's chain of lookups
-// serves many vectors. (One fewer left a second wave of a few CTAs.)
+// Tokens per CTA: as few as fill the SMs' CTAs at most once, and up to so many vectors of K that the chain of lookups is a
+// small part of a CTA's life (one head of 128, token scales: 22.5 us for a write of 110K tokens, 24.6 us with 16 tokens per
+// CTA). More than that leaves an uneven end: reads of whole prompts with 64 tokens of 8 heads took 213 us, not 197.
+constexpr int kVectorsPerCta = 2048;
+
 MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k, long long k_stride, const void* v,
                    long long v_stride, int ctas_per_sm) {
   MoveArgs a;
@@ -427,7 +447,8 @@ MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k,
   a.vecs = g.Hkv * g.d / kVec;
   a.vecs_inv = (uint32_t)(((1ull << 32) + a.vecs - 1) / a.vecs);
   const int ctas = 148 * ctas_per_sm, per = (int)(((long long)g.total_tokens + ctas - 1) / ctas);
-  a.tokens = per > kMaxTokensPerCta ? kMaxTokensPerCta : per;
+  const int most = kVectorsPerCta / a.vecs < kMaxTokensPerCta ? kVectorsPerCta / a.vecs : kMaxTokensPerCta;
+  a.tokens = per > most ? (most > 1 ? most : 1) : per;
   return a;
 }
 
