@@ -173,7 +173,8 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t total = t.total_tokens, d = c->head_dim;
     if (!is_int32(cu, dev, c->batch + 1))
       refuse(fn, "cu_tokens must be a contiguous int32 [" + std::to_string(c->batch + 1) + "] on " + cuda_name(dev));
-    if (!is_rows(q, dev, total, t.hq, d))
+    // (a stride of 0, of an expanded tensor, would mean packed rows to the library)
+    if (!is_rows(q, dev, total, t.hq, d) || (total > 1 && q.stride(0) == 0))
       refuse(fn, "q must be bfloat16 " + shape3(total, t.hq, d) + " on " + cuda_name(dev) + ", contiguous within a token");
     if (!is_rows(o, dev, total, t.hq, d) || !o.is_contiguous())
       refuse(fn, "o must be contiguous bfloat16 " + shape3(total, t.hq, d) + " on " + cuda_name(dev));

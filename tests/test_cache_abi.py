@@ -193,3 +193,16 @@ def test_native_calls_check_before_any_cuda_call(lib):
         fb.fp_cache_write(cache, [0, 1, 3], k, k)
     with pytest.raises(TypeError):
         fb.fp_cache_write(cache, c.cu, k, None)
+
+
+def test_native_tree_refuses_rows_repeated_by_a_zero_stride(lib):
+    """A token stride of 0 means "packed" to the C call, so an expanded q must not reach it."""
+    c = Case([5, 9], [1, 2], hkv=2, G=2, seed=3)
+    cache = fb.Cache(c.pool["k"], c.pool["v"], c.table, c.kv_lens)
+    t = tree(hq=4, total_tokens=3, max_tokens=2)
+    q = torch.zeros(1, 4, 128, dtype=torch.bfloat16).expand(3, 4, 128)
+    o = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q must be"):
+        fb._native().tree_attention(cache.addr, -1, ctypes.addressof(t), 0, 0, c.cu, q, o, None, None, None)
+    with pytest.raises(ValueError, match="o must be"):
+        fb._native().tree_attention(cache.addr, -1, ctypes.addressof(t), 0, 0, c.cu, o, q, None, None, None)
