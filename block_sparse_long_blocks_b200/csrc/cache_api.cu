@@ -165,6 +165,11 @@ fp_status_t fp_tree_attention(const fp_cache_t* c, const fp_tree_t* t, const voi
   CacheGeometry g = geometry(c, t->cu_tokens, t->total_tokens);
   if (!workspace || !aligned(workspace, 256) || ws_bytes < tree_workspace(g, t->hq, t->max_tokens))
     return FP_ERR_WORKSPACE;
+  // CTAs write rows of o while others still read q
+  const long long row = (long long)t->hq * c->head_dim, rows = t->total_tokens - 1;
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  const uintptr_t q_bytes = 2 * (rows * (t->q_stride ? t->q_stride : row) + row), o_bytes = 2 * (rows + 1) * row;
+  if (o0 < q0 + q_bytes && q0 < o0 + o_bytes) return FP_ERR_INVALID_ARG;
   if (!(g.status = status_ptr())) return cuda_fail("device status symbol", cudaGetLastError());
   return launch_tree(g, *t, q, o, lse, workspace, static_cast<cudaStream_t>(stream));
 }

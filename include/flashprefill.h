@@ -362,8 +362,9 @@ size_t fp_tree_workspace_size(const fp_cache_t* c, const fp_tree_t* t);
  * The keys of all requests are divided evenly over the SMs; partial results
  * are combined in a fixed order, so equal calls give equal bits.
  * A request with n_r > max_tokens sets FP_DEV_BAD_SEQLENS and is skipped.
- * o and lse overlap neither q nor the cache. Positions stay below 2^31 - 1024
- * (max_pages_per_req * page_size, else FP_ERR_UNSUPPORTED).
+ * o and lse overlap neither q (o on q: FP_ERR_INVALID_ARG) nor the cache.
+ * Positions stay below 2^31 - 1024 (max_pages_per_req * page_size, else
+ * FP_ERR_UNSUPPORTED).
  * workspace: fp_tree_workspace_size bytes, 256-byte aligned, contents
  * overwritten; calls that may overlap on the GPU need one each.
  */

@@ -206,3 +206,16 @@ def test_native_tree_refuses_rows_repeated_by_a_zero_stride(lib):
         fb._native().tree_attention(cache.addr, -1, ctypes.addressof(t), 0, 0, c.cu, q, o, None, None, None)
     with pytest.raises(ValueError, match="o must be"):
         fb._native().tree_attention(cache.addr, -1, ctypes.addressof(t), 0, 0, c.cu, o, q, None, None, None)
+
+
+@pytest.mark.parametrize("total,stride,off,code", [
+    (6, 0, 0, INVALID), (6, 0, 6 * 32 * 128 * 2 - 16, INVALID), (6, 0, 16 - 6 * 32 * 128 * 2, INVALID),
+    (6, 6144, 32 * 128 * 2, INVALID), (6, 0, 6 * 32 * 128 * 2, None), (6, 0, -6 * 32 * 128 * 2, None),
+    (1, 6144, 32 * 128 * 2, None)])
+def test_tree_output_does_not_overlap_q(lib, total, stride, off, code):
+    c, t = ctypes.byref(cache()), ctypes.byref(tree(hq=32, total_tokens=total, q_stride=stride))
+    ws = lib.fp_tree_workspace_size(c, t)
+    Q = P + (1 << 24)
+    # (no workspace where the call would be let through: nothing is launched either way)
+    got = lib.fp_tree_attention(c, t, Q, Q + off, None, P if code else None, ws, None)
+    assert got == (code if code else WORKSPACE)
