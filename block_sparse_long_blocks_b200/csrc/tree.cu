@@ -40,8 +40,11 @@
 // lies in [2^7, 2^8)) as hi + 2^-5 lo, two e4m3 values whose sum is q exactly for
 // every element within 2^-15 of the largest; up to 8 rows both fill one M tile.
 // V is widened exactly to f16; p carries a factor 2^kShift into f16's normal
-// range. Token scales of V multiply p, divided by a running power of two >= the
-// largest v_scale so far, so p stays within f16.
+// range. Token scales of V multiply p, and f16 holds the product p v_scale
+// relative to the row's own largest one so far (its logarithm's reference is kept
+// beside the softmax's): a reference shared by the rows would let the scale of a
+// key that a row does not see, or hardly weighs, push that row's weights below
+// f16. It costs a multiply-add and a maximum per score.
 // Every wait is bounded; after one ran out the consumers go on without waiting
 // (their loops have fixed lengths, so they still meet at every barrier) and
 // release no slot any more: its copy may be in flight. The producer stops and
@@ -382,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     float v_mul = 1.f;  // what O is multiplied by at the end
     if (E4M3 && !TOKEN) v_mul = __ldg(g.v_scale + sg.head);
+    // what O is relative to where that is not ref (TOKEN): a maximum of x + log2(v_scale)
+    [[maybe_unused]] float vref[NB];
 
     float o[MT][NB][4];  // columns 16 mt + gr (elements 0, 1) and + 8 (2, 3) of rows 8 b + 2c + {0, 1}
 #pragma unroll
@@ -394,10 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float ref[NB], l[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      ref[b] = -INFINITY;
+      ref[b] = vref[b] = -INFINITY;
       l[b] = 0.f;
     }
-    uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
 
     // STEPS blocks of 16 keys of one tile: first position pos0, first key k0 of the
     // tile; SPECIAL: some are new tokens, or slots behind the last one.
@@ -493,6 +497,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
 
+      if (TOKEN && ok) ok = mbar_wait<true>(vfull, vphase, abort_flag, g.status, FP_DEV_TIMEOUT);
+      bool odd = false;  // a new token's V or scale is an infinity or NaN
+      [[maybe_unused]] float2 vf[STEPS][2];   // token scales of V, times 2^-kScaleShift
+      [[maybe_unused]] float vmx[NB];         // maximum of x + log2(v_scale)
+      if constexpr (TOKEN) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vmx[b] = -INFINITY;
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const int key = st * 16 + (nt ? key1 : key0);
+            float2 y = *reinterpret_cast<const float2*>(vsc + k0 + key);
+            if constexpr (SPECIAL) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& f = e ? y.y : y.x;
+                const int pos = pos0 + key + e;
+                if (pos >= sg.kv) {
+                  f = 0.f;  // (whatever the slot held before: times a weight of zero it may be NaN)
+                } else if (pos >= sg.base && !(f < INFINITY)) {
+                  odd = true;
+                  f = 0.f;
+                }
+              }
+            }
+            const float lx = scale_log2(y.x), ly = scale_log2(y.y);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              vmx[b] = fmaxf(vmx[b], fmaxf(fmaf(s[st][b][nt][0], sl2[b], lx), fmaf(s[st][b][nt][1], sl2[b], ly)));
+            vf[st][nt] = make_float2(y.x * kScaleDown, y.y * kScaleDown);
+          }
+      }
+
       // ---- softmax
       bool grew = false;
 #pragma unroll
@@ -500,6 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 1));
         mx[b] = fmaxf(mx[b], __shfl_xor_sync(0xffffffffu, mx[b], 2)) * sl2[b];
         grew |= mx[b] > ref[b] + kSlack;
+        if constexpr (TOKEN) {
+          vmx[b] = fmaxf(vmx[b], __shfl_xor_sync(0xffffffffu, vmx[b], 1));
+          vmx[b] = fmaxf(vmx[b], __shfl_xor_sync(0xffffffffu, vmx[b], 2));
+          grew |= vmx[b] > vref[b] + kSlack;
+        }
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -510,6 +553,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ref[b] = mx[b];
           }
           l[b] *= f;
+          if constexpr (TOKEN) {
+            f = 1.f;
+            if (vmx[b] > vref[b] + kSlack) {
+              f = exp2_fast(vref[b] - vmx[b]);
+              vref[b] = vmx[b];
+            }
+          }
           // O's columns are rows 2c and 2c + 1 of the block
           const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
 #pragma unroll
@@ -523,69 +573,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int b = 0; b < NB; ++b) neg[b] = ref[b] == -INFINITY ? 0.f : (E4M3 ? kShift - ref[b] : -ref[b]);
 
-      if (ok) ok = mbar_wait<true>(vfull, vphase, abort_flag, g.status, FP_DEV_TIMEOUT);
-      [[maybe_unused]] float inv_ref = 1.f;
+      if (!TOKEN && ok) ok = mbar_wait<true>(vfull, vphase, abort_flag, g.status, FP_DEV_TIMEOUT);
+      [[maybe_unused]] float to_v[NB];  // from weights relative to ref to products relative to vref
       if constexpr (TOKEN) {
-        // the largest v_scale of these keys (scales are not negative: they compare as integers)
-        uint32_t top = 0;
-        if (STEPS == 2 || lane < 16) top = __float_as_uint(vsc[k0 + lane]);
-        if constexpr (SPECIAL) {  // not those of slots behind the last token, or of new tokens without a finite one
-          const int pos = pos0 + lane;
-          if (pos >= sg.kv || (pos >= sg.base && top >= 0x7f800000u)) top = 0;
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        // the next power of two above it, within 2^-100 .. 2^127
-        const uint32_t need = top == 0 ? 0 : min(max((top >> 23) + 1u, 27u), 254u);
-        if (need > v_exp) {  // (the whole warp agrees)
-          if (v_exp != 0) {
-            const float k = exp2_fast((float)((int)v_exp - (int)need));
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][b][e] *= k;
-          }
-          v_exp = need;
-        }
-        // 2^-(v_exp - 127); where every scale so far was zero it does not matter
-        inv_ref = __uint_as_float((v_exp == 254u ? 1u : 254u - max(v_exp, 27u)) << 23);
-        if (v_exp == 254u) inv_ref *= 0.5f;
+        for (int b = 0; b < NB; ++b) to_v[b] = products_factor(ref[b], vref[b]);
       }
       uint32_t pf[STEPS][NB][2], pl[STEPS][NB][2];
-      bool odd = false;  // a new token's V or scale is an infinity or NaN
 #pragma unroll
       for (int st = 0; st < STEPS; ++st)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-          float2 vf = make_float2(1.f, 1.f);
-          if constexpr (TOKEN) {
-            const int key = st * 16 + (nt ? key1 : key0);
-            vf = *reinterpret_cast<const float2*>(vsc + k0 + key);
-            if constexpr (SPECIAL) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& y = e ? vf.y : vf.x;
-                const int pos = pos0 + key + e;
-                if (pos >= sg.kv) {
-                  y = 0.f;  // (whatever the slot held before: times a weight of zero it may be NaN)
-                } else if (pos >= sg.base && !(y < INFINITY)) {
-                  odd = true;
-                  y = 0.f;
-                }
-              }
-            }
-            vf.x *= inv_ref;
-            vf.y *= inv_ref;
-          }
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             float p0 = exp2_fast(fmaf(s[st][b][nt][0], sl2[b], neg[b]));
             float p1 = exp2_fast(fmaf(s[st][b][nt][1], sl2[b], neg[b]));
             l[b] += p0 + p1;
             if constexpr (TOKEN) {
-              p0 *= vf.x;
-              p1 *= vf.y;
+              p0 = p0 * vf[st][nt].x * to_v[b];
+              p1 = p1 * vf[st][nt].y * to_v[b];
             }
             const uint32_t u = pack2<E4M3>(p0, p1);
             pf[st][b][nt] = u;
@@ -677,7 +683,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_l[warp * C::ROWS + gr + 8 * b] = l[b];
       }
     }
-    if (TOKEN) v_mul = v_exp == 0 ? 0.f : __uint_as_float(v_exp << 23);
     consumers_sync();
     if (threadIdx.x == 0) s_odd[(segment + 1) & 1] = 0;  // (its readers have passed the barrier above)
     const bool whole = sg.whole();
@@ -696,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum += pl2[k * C::ROWS] * (big == -INFINITY ? 1.f : exp2_fast(pm[k * C::ROWS] - big));
       float w = big == -INFINITY ? 1.f : exp2_fast(ref[b] - big);
       w = sum == 0.f ? 0.f : __fdividef(w * v_mul, sum);
+      if constexpr (TOKEN) w = products_back(big, vref[b], sum);  // (NaN without a maximum: then so is the sum)
       top[b] = big;
       all[b] = sum;
       const float w0 = __shfl_sync(0xffffffffu, w, 8 * c), w1 = __shfl_sync(0xffffffffu, w, 8 * c + 4);
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float we = (e & 1) ? w1 : w0;
-          o[i][b][e] = we == 0.f ? 0.f : o[i][b][e] * we;
+          o[i][b][e] = we == 0.f ? 0.f : TOKEN ? o[i][b][e] * we * we : o[i][b][e] * we;
         }
     }
     const bool odd = s_odd[segment & 1] != 0;

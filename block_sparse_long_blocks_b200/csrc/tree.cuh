@@ -226,6 +226,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Token scales of V. A weight p = 2^(x - ref + kShift) times v_scale goes to f16 as
+//   p (v_scale 2^-kScaleShift) 2^(ref - vref + kScaleShift) = 2^(x + log2 v_scale - vref + kShift)
+// with vref, as ref, a row's maximum of x + log2 v_scale at its last rise: at most 2^15, whatever the scales of keys
+// that the row does not see. The shift keeps both products within float32 for scales up to its largest value and
+// rows whose scales are all tiny. Scales below 2^-100 count as 2^-100 here (their products just stay smaller).
+constexpr float kScaleShift = 16.f, kScaleDown = 0x1p-16f;
+__device__ __forceinline__ float scale_log2(float v) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  return fminf(fmaxf(y, -100.f), 128.f);  // (of NaN -100: what it enters becomes NaN by the scale itself)
+}
+__device__ __forceinline__ float products_factor(float ref, float vref) {
+  return vref == -INFINITY ? 0.f : exp2_fast(ref - vref + kScaleShift);
+}
+// O relative to vref becomes O / sum, with sum relative to ref, by two multiplications with this factor (one with its square
+// could leave float32's range). Zero where a row saw nothing.
+__device__ __forceinline__ float products_back(float ref, float vref, float sum) {
+  return sum == 0.f ? 0.f : exp2_fast(0.5f * (vref - ref)) * rsqrtf(sum);
+}
+
 // Two float32 -> two e4m3 codes (the first in the low byte), nearest even, NaN stays NaN.
 __device__ __forceinline__ uint32_t pack_codes(float a, float b) {
   unsigned short h;

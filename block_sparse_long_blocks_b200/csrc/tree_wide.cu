@@ -67,7 +67,8 @@ struct Roles {
 constexpr int kKeys = 128;           // per tile
 constexpr int kChunk = kKeys * 128;  // bytes of a tile's 128-byte-wide chunk
 constexpr int kFlags = 8;            // > segments that the ring can reach into
-constexpr int kScales = 8;           // tiles whose token scales are kept (see the producer)
+constexpr int kScales = 8;           // tiles whose token scales are kept (see the producer),
+constexpr int kLogs = 4;             // and the logarithms of V's (see the converters)
 
 template <bool E4M3, int D, bool PAIR>
 struct Cfg {
@@ -86,9 +87,10 @@ struct Cfg {
   static constexpr int M_SLOTS = E4M3 ? W_SLOTS : V_SLOTS;  // V tiles as multiplied
   static constexpr int AHEAD = PAIR ? 1 : 2;            // K tiles loaded before the first V tile; tiles from one
                                                         // of a warpgroup to its next
-  static constexpr int NUM_BARS = 2 * K_SLOTS + 2 * V_SLOTS + 2 * M_SLOTS + 2 + 2 + 4 + 2 + 6;
+  static constexpr int NUM_BARS = 2 * K_SLOTS + 2 * V_SLOTS + 2 * M_SLOTS + 2 + 2 + 4 + 2 + 6 + kLogs;
   static constexpr int SMEM_FIXED = 1024 + Q + (K_SLOTS + V_SLOTS) * LOAD + W_SLOTS * TILE +
-                                    (E4M3 ? (kScales * 2 + 1) * kKeys * 4 : 0) + 256 * 16 + 1024 + NUM_BARS * 8 + 336;
+                                    (E4M3 ? (kScales * 2 + kLogs + 1) * kKeys * 4 : 0) + 256 * 16 + 1024 + NUM_BARS * 8 +
+                                    336;
   // columns of O that either of two warpgroups hands the other through Q's place at a time
   static constexpr int COLS = Q1 / 1024;
   static_assert(SMEM_FIXED + kAxisBytesMax <= 227 * 1024, "shared memory");
@@ -129,7 +131,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   uint8_t* sM = E4M3 ? sW : sV;                  // V tiles as multiplied
   float* s_ksc = reinterpret_cast<float*>(sW + C::W_SLOTS * C::TILE);  // [kScales][kKeys]
   float* s_vsc = s_ksc + (E4M3 ? kScales * kKeys : 0);
-  float* s_ones = s_vsc + (E4M3 ? kScales * kKeys : 0);                // [kKeys] (TOKEN)
+  float* s_vlog = s_vsc + (E4M3 ? kScales * kKeys : 0);                // [kLogs][kKeys]: log2 of V's scales (TOKEN)
+  float* s_ones = s_vlog + (E4M3 ? kLogs * kKeys : 0);                 // [kKeys] (TOKEN)
   float4* s_half = reinterpret_cast<float4*>(s_ones + (E4M3 ? kKeys : 0));  // [2][128] the warpgroups' sums
   float* s_back = reinterpret_cast<float*>(s_half + 256);                   // [2][128] factors of Q's rows (e4m3)
   uint64_t* k_full = reinterpret_cast<uint64_t*>(s_back + 256);
@@ -146,10 +149,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
   uint64_t* half_empty = half_full + 1;
   uint64_t* drain = half_empty + 1;               // [2]
   uint64_t* turn = drain + 2;                     // [2] (PAIR)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
+  uint64_t* log_full = turn + 2;                  // [kLogs] V's scales are clean, with their logarithms (TOKEN)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(log_full + kLogs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* warp_sum = reinterpret_cast<int*>(tmem_slot + 2);             // [16]
-  volatile uint32_t* s_vmax = tmem_slot + 18;                        // [kScales][2]
+  volatile uint32_t* s_vmax = tmem_slot + 18;                        // [kLogs][2]: V's largest scales, as bits (TOKEN)
   volatile int* s_odd = reinterpret_cast<volatile int*>(tmem_slot + 50);  // [kFlags][4]
   Axis axis(tmem_slot + 84, a.g.R);
 
@@ -181,6 +185,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       mbar_init(drain + w, 1);
       mbar_init(turn + w, 1);
     }
+    for (int s = 0; s < kLogs; ++s) mbar_init(log_full + s, L::CONVERTERS);
     mbar_init(half_full, 256);
     mbar_init(half_empty, 256);
     *abort_flag = 0;
@@ -409,11 +414,39 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             }
           }
         } else {
+          if constexpr (TOKEN) {
+            // The softmax needs the scales before the products with V need the tile, so they are out before the wait for
+            // its place. Tile n's logarithms replace those of n - 4, whose softmax is over: V n is here, so V n - 2 and
+            // V n - 3 are converted, which followed the products with V n - 4 and V n - 5. Whoever waits for tile n of
+            // log_full has its scores, which follow the products with V n - 4, and n + 4 comes after those with V n.
+            float2& at = reinterpret_cast<float2*>(s_vsc + tn % kScales * kKeys)[ct];  // (two keys per converter)
+            float2 sc = at;
+            if (special) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& y = e ? sc.y : sc.x;
+                const int pos = pos0 + 2 * ct + e;
+                if (pos >= sg.kv) {
+                  y = 0.f;
+                } else if (pos >= sg.base && !(y < INFINITY)) {
+                  y = 0.f;
+                  odd = true;
+                }
+              }
+            }
+            at = make_float2(sc.x * kScaleDown, sc.y * kScaleDown);
+            reinterpret_cast<float2*>(s_vlog + tn % kLogs * kKeys)[ct] = make_float2(scale_log2(sc.x), scale_log2(sc.y));
+            // (scales are not negative: they compare as integers)
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(sc.x), __float_as_uint(sc.y)));
+            if (lane == 0) s_vmax[tn % kLogs * 2 + (cw & 1)] = top;
+            mbar_arrive(log_full + tn % kLogs);
+          }
           ok = mbar_wait<true>(m_empty + ms, ((uint32_t)(tn / C::M_SLOTS) & 1u) ^ 1u, abort_flag, g.status,
                                FP_DEV_TIMEOUT);
           if (!ok) break;
           const uint8_t* src = sV + vs * C::LOAD;
-#pragma unroll 4
+          constexpr int U = TOKEN ? 2 : 4;  // (more would spill: 235 us, not 223, 64 tokens over 128K keys)
+#pragma unroll U
           for (int q = ct; q < kKeys * 8; q += L::CONVERTERS) {
             // eight threads take four granules each of keys k and k ^ 5: their 16-byte places differ in the swizzled
             // row that is read and in the two that are written
@@ -434,27 +467,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
                 make_uint4(widen_lo(w.x), widen_hi(w.x), widen_lo(w.y), widen_hi(w.y));
             *reinterpret_cast<uint4*>(row + (((p + 1) ^ sw) << 4)) =
                 make_uint4(widen_lo(w.z), widen_hi(w.z), widen_lo(w.w), widen_hi(w.w));
-          }
-          if constexpr (TOKEN) {
-            float2& at = reinterpret_cast<float2*>(s_vsc + tn % kScales * kKeys)[ct];  // (two keys per converter)
-            float2 sc = at;
-            if (special) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& y = e ? sc.y : sc.x;
-                const int pos = pos0 + 2 * ct + e;
-                if (pos >= sg.kv) {
-                  y = 0.f;
-                } else if (pos >= sg.base && !(y < INFINITY)) {
-                  y = 0.f;
-                  odd = true;
-                }
-              }
-              at = sc;
-            }
-            // (scales are not negative: they compare as integers)
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(sc.x), __float_as_uint(sc.y)));
-            if (lane == 0) s_vmax[tn % kScales * 2 + (cw & 1)] = top;
           }
         }
         if (odd) s_odd[segment % kFlags * 4 + cw] = segment + 1;
@@ -562,11 +574,12 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       }
       float v_mul = 1.f;  // what O is multiplied by at the end
       if (E4M3 && !TOKEN) v_mul = __ldg(g.v_scale + sg.head);
+      // what O is relative to where that is not ref (TOKEN, see products_factor): a maximum of x + log2(v_scale)
+      [[maybe_unused]] float vref = -INFINITY;
 
       // l: the sum of the weights; lu: of the weights as they are multiplied with V (bf16), by which O is
       // divided, so that O stays an average of V rows whatever the rounding
       float ref = -INFINITY, l = 0.f, lu = 0.f;
-      uint32_t v_exp = 0;  // token scales: exponent field of the power of two above the largest v_scale so far
       const bool any_rows = __any_sync(0xffffffffu, in);
       const int first = PAIR ? 0 : (w - tn) & 1;
       for (int i = first; i < nt; i += C::AHEAD) {
@@ -637,23 +650,38 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           l *= f;
           lu *= f;
         }
-        float inv_ref = 1.f;
+        [[maybe_unused]] float to_v = 1.f;
         if constexpr (TOKEN) {
-          const int ms = (tn + i) % C::M_SLOTS;  // V's scales are there once it is converted
-          ok = mbar_wait<true>(m_full + ms, (uint32_t)((tn + i) / C::M_SLOTS) & 1u, abort_flag, g.status,
-                               FP_DEV_TIMEOUT);
+          const int at = (tn + i) % kLogs;
+          ok = mbar_wait<true>(log_full + at, (uint32_t)((tn + i) / kLogs) & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
           if (!ok) break;
-          const int at = (tn + i) % kScales;
-          const uint32_t top = max(s_vmax[at * 2], s_vmax[at * 2 + 1]);
-          // the next power of two above it, within 2^-100 .. 2^127
-          const uint32_t need = top == 0 ? 0 : min(max((top >> 23) + 1u, 27u), 254u);
-          if (need > v_exp) {  // (all threads agree)
-            if (v_exp != 0) f *= exp2_fast((float)((int)v_exp - (int)need));
-            v_exp = need;
+          f = 1.f;
+          // The tile's largest scale bounds x + log2(v_scale): the exact maxima are only formed where some row's reference
+          // may have to rise, which they decide (a half more than covers the roundings; formed for every tile: 255 us where
+          // this takes 223 us, 64 tokens of 8 query heads over 128K keys).
+          const float most = mx + scale_log2(__uint_as_float(max(s_vmax[at * 2], s_vmax[at * 2 + 1])));
+          if (__any_sync(0xffffffffu, most + 0.5f > vref + kSlack)) {
+            float v0 = -INFINITY, v1 = -INFINITY;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kKeys; c0 += 16) {
+              float x[16];
+              tmem_ld16(tS + c0, reinterpret_cast<uint32_t(&)[16]>(x));
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 16; c += 4) {
+                const float4 k = *reinterpret_cast<const float4*>(ksc + c0 + c);
+                const float4 lg = *reinterpret_cast<const float4*>(s_vlog + at * kKeys + c0 + c);
+                v0 = max3(v0, fmaf(x[c] * k.x, sl2, lg.x), fmaf(x[c + 1] * k.y, sl2, lg.y));
+                v1 = max3(v1, fmaf(x[c + 2] * k.z, sl2, lg.z), fmaf(x[c + 3] * k.w, sl2, lg.w));
+              }
+            }
+            const float vmx = fmaxf(v0, v1);
+            if (vmx > vref + kSlack) {
+              f = exp2_fast(vref - vmx);
+              vref = vmx;
+            }
           }
-          // 2^-(v_exp - 127); where every scale so far was zero it does not matter
-          inv_ref = __uint_as_float((v_exp == 254u ? 1u : 254u - max(v_exp, 27u)) << 23);
-          if (v_exp == 254u) inv_ref *= 0.5f;
+          to_v = products_factor(ref, vref);
         }
         if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
@@ -667,7 +695,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
           }
         }
         const float neg = ref == -INFINITY ? 0.f : (E4M3 ? kShift - ref : -ref);
-        const uint64_t sl2x2 = f2_pack(sl2, sl2), negx2 = f2_pack(neg, neg), invx2 = f2_pack(inv_ref, inv_ref);
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), negx2 = f2_pack(neg, neg);
+        [[maybe_unused]] const uint64_t to_vx2 = f2_pack(to_v, to_v);
         uint64_t sum0 = 0, sum1 = 0, used0 = 0, used1 = 0;  // (pairs of float32 zeros)
         const float* vsc = s_vsc + (tn + i) % kScales * kKeys;
         // P goes out in two halves of the keys; O += P V starts on the first while the second is computed
@@ -687,7 +716,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             else sum0 = f2_add(sum0, p);
             if constexpr (TOKEN) {
               const float2 vs = *reinterpret_cast<const float2*>(vsc + hf * 64 + 2 * e);
-              f2_unpack(f2_mul(f2_mul(p, f2_pack(vs.x, vs.y)), invx2), p0, p1);
+              f2_unpack(f2_mul(f2_mul(p, f2_pack(vs.x, vs.y)), to_vx2), p0, p1);
             }
             p16[e] = pack2<E4M3>(p0, p1);
             if constexpr (!E4M3) {
@@ -713,7 +742,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       }
       if (E4M3) lu = l;
       if (!ok) break;
-      if (TOKEN) v_mul = v_exp == 0 ? 0.f : __uint_as_float(v_exp << 23);
       ok = mbar_wait<true>(o_full + w, (uint32_t)on & 1u, abort_flag, g.status, FP_DEV_TIMEOUT);
       if (!ok) break;
       ++on;
@@ -772,7 +800,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       };
       if (PAIR || nt == 1) {
         if ((PAIR || first == 0) && any_rows) {
-          const float f = lu == 0.f ? 0.f : v_mul / lu;
+          const float f = TOKEN ? products_back(ref, vref, l) : lu == 0.f ? 0.f : v_mul / lu;
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
             if (hf * 16 >= rows_in) break;
@@ -784,7 +812,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
               tmem_ld_frag16(tO + (hf << 20) + c0 + 16, o + 8);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= (e & 2) ? f1 : f0;
+              for (int e = 0; e < 16; ++e) {
+                const float fe = (e & 2) ? f1 : f0;
+                o[e] = TOKEN ? o[e] * fe * fe : o[e] * fe;
+              }
               store16(o, hf, c0);
               store16(o + 8, hf, c0 + 16);
             }
@@ -794,7 +825,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
       } else {
         // Either warpgroup finishes half of the columns: the other's O comes through Q's place (its products are over)
         // in rounds of COLS columns, every thread's fragments to the same thread of the other.
-        s_half[w * 128 + row] = make_float4(ref, l, v_mul, lu);
+        s_half[w * 128 + row] = make_float4(ref, l, TOKEN ? vref : v_mul, lu);
         float* box = reinterpret_cast<float*>(sQ) + (threadIdx.x & 127) * 4;  // [2][COLS / 4 pieces][128][4]
         constexpr int PIECES = C::COLS / 4;
         float top = 0.f, sum = 0.f, mine = 0.f, theirs = 0.f;
@@ -826,8 +857,13 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             const float e1 = top == -INFINITY ? 1.f : exp2_fast(y.x - top);
             sum = l * e0 + y.y * e1;
             const float used = lu * e0 + y.w * e1;
-            mine = used == 0.f ? 0.f : e0 * v_mul / used;
-            theirs = used == 0.f ? 0.f : e1 * y.z / used;
+            if constexpr (TOKEN) {  // (NaN where neither has a maximum: then so is `used`, or zero)
+              mine = products_back(top, vref, used);
+              theirs = products_back(top, y.z, used);
+            } else {
+              mine = used == 0.f ? 0.f : e0 * v_mul / used;
+              theirs = used == 0.f ? 0.f : e1 * y.z / used;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               fm[k] = __shfl_sync(0xffffffffu, mine, 8 * k + fr);
@@ -847,7 +883,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
                 const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = o[e] * fm[2 * hf + ((e >> 1) & 1)] + y[e] * ft[2 * hf + ((e >> 1) & 1)];
+                for (int e = 0; e < 8; ++e) {
+                  const float f = fm[2 * hf + ((e >> 1) & 1)], g = ft[2 * hf + ((e >> 1) & 1)];
+                  o[e] = TOKEN ? o[e] * f * f + y[e] * g * g : o[e] * f + y[e] * g;
+                }
                 store16(o, hf, keep + c);
               }
           }
