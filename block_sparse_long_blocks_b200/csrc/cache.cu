@@ -116,6 +116,14 @@ __device__ __forceinline__ void unpack_bf16(uint32_t u, float& a, float& b) {
   b = __uint_as_float(u & 0xffff0000u);
 }
 
+// ... with their signs turned, in as many instructions (the low one's sign by the addition)
+__device__ __forceinline__ void unpack_minus(uint32_t u, float& a, float& b) {
+  uint32_t lo;
+  asm("mad.lo.u32 %0, %1, 65536, 0x80000000;" : "=r"(lo) : "r"(u));
+  a = __uint_as_float(lo);
+  b = __uint_as_float((u & 0xffff0000u) ^ 0x80000000u);
+}
+
 // Two float32 -> two e4m3 codes (the first in the low byte), round to nearest
 // even, saturating at +-448; NaN stays NaN.
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
@@ -139,30 +147,32 @@ __device__ __forceinline__ Divisor divisor(float scale) {
 // multiply-add), q + r y is the correctly rounded quotient (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990): three packed instructions for two elements. The general division took
-// about twelve each and set the pace (4.2 of the 6.5 TB/s).
+// about twelve each and set the pace (4.2 of the 6.5 TB/s). Computed from -x as
+// q = (-x)(-y), -r = q s + (-x), q + (-r)(-y): of x = -0 the other signs would
+// make +0 (-r = +0 either way, and (+0)(-y) = -0 leaves q's sign).
 // BOUNDED: no |x| exceeds 448 s.
 template <bool BOUNDED>
 __device__ __forceinline__ uint2 quantise(const uint4& in, const Divisor& d) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
   uint32_t code[4];
-  const uint64_t y = f2_pack(d.inv, d.inv), ns = f2_pack(-d.scale, -d.scale);
+  const uint64_t ny = f2_pack(-d.inv, -d.inv), s = f2_pack(d.scale, d.scale);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a, b;
-    unpack_bf16(w[i], a, b);
+    float a, b;  // -x
+    unpack_minus(w[i], a, b);
     float qa, qb;
     if (d.plain) {
-      const uint64_t x = f2_pack(a, b), q = f2_mul(x, y);
+      const uint64_t nx = f2_pack(a, b), q = f2_mul(nx, ny);
       float pa, pb;
       f2_unpack(q, pa, pb);
-      f2_unpack(f2_fma(f2_fma(q, ns, x), y, q), qa, qb);
+      f2_unpack(f2_fma(f2_fma(q, s, nx), ny, q), qa, qb);
       if constexpr (!BOUNDED) {  // far beyond the largest code the estimate does, and the correction may overflow
         qa = fabsf(pa) < 1024.f ? qa : pa;
         qb = fabsf(pb) < 1024.f ? qb : pb;
       }
     } else {
-      qa = __fdiv_rn(a, d.scale);
-      qb = __fdiv_rn(b, d.scale);
+      qa = __fdiv_rn(a, -d.scale);
+      qb = __fdiv_rn(b, -d.scale);
     }
     code[i] = pack_e4m3(qa, qb);
   }

@@ -114,6 +114,28 @@ def test_write_values_where_quantising_can_go_wrong(fmt):
     check_cache(c, want)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3_head", "e4m3_token"])
+def test_write_keeps_the_sign_of_zero(fmt):
+    """-0.0 alone, beside ordinary values, and values so small that they become -0: codes 0x80, whatever the scale."""
+    c = Case([6], [6], hkv=3, page=16, fmt=fmt)
+    if fmt == "e4m3_head":
+        for name in "kv":
+            c.scale[name] = torch.tensor([0.37, 2.0 ** -100, 0.0])  # in and out of the correction's range; 0: taken as 1
+    c.cuda()
+    rows = packed_rows(c, spread=False)
+    for x in rows:
+        x[0] = -0.0
+        x[1, :, ::3] = -0.0
+        x[2] = x[2].abs() * 2.0 ** -120
+        x[2, :, 1::2] = -0.0
+        x[3, :, 5:] *= 2.0 ** -60
+        x[4] = 0.0
+    want = written(c, rows)
+    fb.fp_cache_write(c.cache, c.gpu["cu"], rows[0].cuda(), rows[1].cuda())
+    check_cache(c, want)
+    assert (bits8(want[0]["k"]).flatten(0, 1)[c.new_slots(0)[:1]] == 0x80).all()
+
+
 def test_write_keeps_nan_where_it_is():
     c = Case([4], [4], hkv=1, page=16, fmt="e4m3_token").cuda()
     rows = packed_rows(c, spread=False)
