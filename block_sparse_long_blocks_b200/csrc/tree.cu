@@ -746,6 +746,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 hi = odd_values<E4M3, TOKEN, D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0, end, t, d + 2);
           acc = make_float4(acc.x + lo.x, acc.y + lo.y, acc.z + hi.x, acc.w + hi.y);
         }
+        if (!E4M3 && isnan((acc.x + acc.y) + (acc.z + acc.w))) {
+          float sum = 0.f;
+          for (int k = 0; k < kWarps; ++k) sum += s_l[k * C::ROWS + lr];
+          if (sum == sum) {
+            const float4 f = infinite_values<D>(a, sg.r, sg.off, sg.head, sg.base, sg.t0 << a.tile_shift,
+                                                min(sg.kv, sg.t1 << a.tile_shift), t, d);
+            acc = make_float4(f.x != 0.f ? f.x : acc.x, f.y != 0.f ? f.y : acc.y, f.z != 0.f ? f.z : acc.z,
+                              f.w != 0.f ? f.w : acc.w);
+          }
+        }
         if (whole) {
           *reinterpret_cast<uint2*>(a.o + ((long long)(sg.off + t) * a.Hq + sg.head * a.G + h) * D + d) =
               make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));

@@ -333,6 +333,41 @@ __device__ __noinline__ float2 odd_values(const TreeArgs& a, int r, int off, int
   return acc;
 }
 
+// bf16 weights enter the product with V as hi + lo, and infinity times a rest lo <= 0 is NaN. Where a row of finite weights
+// got NaN in one of four columns of V: the sums of the infinities and NaN that the keys from .. end - 1 hold there as far as
+// token t sees them (rare; a page's slots in turn, with eight loads in flight, until nothing can change any more).
+template <int D>
+__device__ __noinline__ float4 infinite_values(const TreeArgs& a, int r, int off, int head, int base, int from, int end,
+                                               int t, int d) {
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const CacheGeometry& g = a.g;
+  const int32_t* row = g.table + (long long)r * g.max_pages;
+  for (int p0 = from; p0 < end;) {
+    const int p1 = min(end, (p0 | (g.page_size - 1)) + 1), page = __ldg(row + (p0 >> g.page_shift));
+    if (page >= 0 && page < g.num_pages) {
+      const uint8_t* v = g.v_pool + 2 * ((((long long)page << g.page_shift) * g.Hkv + head) * D + d);
+#pragma unroll 8
+      for (int pos = p0; pos < p1; ++pos) {
+        const uint2 w = *reinterpret_cast<const uint2*>(v + (long long)(pos & (g.page_size - 1)) * g.Hkv * D * 2);
+        const uint32_t m = 0x7f807f80u;
+        if (((__vcmpeq2(w.x & m, m) | __vcmpeq2(w.y & m, m))) == 0) continue;
+        const int j = pos - base;
+        if (j >= 0 &&
+            !(a.mask ? (__ldg(a.mask + (long long)(off + t) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u : j <= t))
+          continue;
+        const float f[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                            __uint_as_float(w.y & 0xffff0000u)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!isfinite(f[e])) acc[e] += f[e];
+      }
+    }
+    if (isnan(acc[0]) && isnan(acc[1]) && isnan(acc[2]) && isnan(acc[3])) break;
+    p0 = p1;
+  }
+  return make_float4(acc[0], acc[1], acc[2], acc[3]);
+}
+
 // Lets a kernel take all the dynamic shared memory a CTA can have, and checks that it was built with the registers
 // per thread that its setmaxnreg split counts on (a larger split would wait for registers for ever): once per kernel
 // and device, as the runtime calls cost a fifth of a launch.

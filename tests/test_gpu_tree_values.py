@@ -1,11 +1,12 @@
-"""fp_tree_attention where V's token scales differ by many orders of magnitude between the keys of a row."""
+"""fp_tree_attention where V's token scales differ by many orders of magnitude between the keys of a row, and where V
+holds infinities and NaN."""
 import numpy as np
 import pytest
 import torch
 
 from block_sparse_long_blocks_b200 import binding as fb
 from oracle import paged_cache as pc
-from tests._cache_helpers import E4M3_MAX, Case
+from tests._cache_helpers import E4M3_MAX, Case, check_tree
 
 pytestmark = pytest.mark.gpu
 # (G, n): 8, 16, 128 and 256 rows per unit
@@ -119,3 +120,35 @@ def test_uneven_scales_over_keys_split_between_ctas(G, n):
     print("of the bound", check_rows(c, o, lse))
     again = c.attend()
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1]) and fb.fp_get_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 256])
+@pytest.mark.parametrize("G,n", KERNELS)
+def test_infinities_of_cached_values_arrive(G, n, page, d):
+    """Infinities of either sign in cached rows, alone and both in a column, beside NaN, and in a new token as well."""
+    c = Case([n + 500, n + 20, n + 70], [n, n, n], hkv=2, G=G, d=d, page=page, fmt="bf16", seed=n).trees()
+    v = c.pool["v"].flatten(0, 1)
+    at = c.flat(0, np.array([3, 130, 131, 400]))
+    v[at[0], :, 5] = float("inf")
+    v[at[1], :, 6] = float("-inf")
+    v[at[[1, 3]], :, 9] = float("inf")
+    v[at[2], 0, 20], v[at[3], 0, 20] = float("inf"), float("-inf")
+    v[at[0], 1, 33], v[at[2], 1, 33] = float("inf"), float("nan")
+    v[c.flat(1, np.array([7])), :, 40] = float("-inf")
+    v[c.new_slots(1)[[1]], :, 40] = float("inf")   # NaN for the rows that see it
+    v[c.new_slots(1)[[1]], :, 41] = float("inf")
+    o, lse = c.cuda().attend()
+    check_tree(c, o, lse)
+    assert torch.isinf(o[:n].float()).any() and fb.fp_get_device_status() == 0
+
+
+def test_infinities_over_keys_split_between_ctas_and_a_query_of_nan():
+    c = Case([9000, 40], [3, 2], hkv=2, G=2, page=64, fmt="bf16", seed=3).trees()
+    v = c.pool["v"].flatten(0, 1)
+    for pos, col, x in ((5, 1, "inf"), (8000, 1, "inf"), (4000, 2, "-inf"), (100, 3, "inf"), (8900, 3, "-inf"), (77, 4, "nan")):
+        v[c.flat(0, np.array([pos])), :, col] = float(x)
+    c.q[1, 3] = float("nan")
+    o, lse = c.cuda().attend()
+    check_tree(c, o, lse)
+    assert fb.fp_get_device_status() == 0
