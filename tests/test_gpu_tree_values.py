@@ -152,3 +152,36 @@ def test_infinities_over_keys_split_between_ctas_and_a_query_of_nan():
     o, lse = c.cuda().attend()
     check_tree(c, o, lse)
     assert fb.fp_get_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3_head", "e4m3_token"])
+@pytest.mark.parametrize("kv", [300, 9000])
+@pytest.mark.parametrize("G,n", KERNELS)
+def test_nan_of_a_value_reaches_a_row_that_hardly_weighs_it(G, n, kv, fmt):
+    """NaN in cached V where the last new token's weight is 2^200 times the others', within a CTA and over many."""
+    c = Case([n + kv], [n], hkv=1, G=G, page=64, fmt=fmt, seed=n)
+    see = np.tril(np.ones((n, n), dtype=bool))
+    see[:, 0] = True
+    c.trees()
+    c.see = see
+    c.mask = torch.from_numpy(np.packbits(np.pad(see, ((0, 0), (0, 64 - n))).reshape(n, 2, 32), axis=-1,
+                                          bitorder="little").view(np.int32).reshape(n, 2).copy())
+    t = 200 * np.sqrt(c.d) * np.log(2.0)
+    k = (t * c.u / c.u.square().sum()).expand(1, c.d)
+    i = c.new_slots(0)[:1]
+    if fmt == "bf16":
+        c.pool["k"].flatten(0, 1)[i] = k.bfloat16()
+    else:
+        sc = k.abs().amax() / E4M3_MAX
+        if fmt == "e4m3_token":
+            c.scale["k"][i // c.page, :, i % c.page] = sc
+        else:
+            c.scale["k"] = torch.maximum(c.scale["k"], sc)  # (the other keys' scores just grow a little)
+            sc = c.scale["k"][0]
+        c.pool["k"].view(torch.uint8).flatten(0, 1)[i] = (k / sc).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.fill("v", c.flat(0, np.array([3])), float("nan"))
+    o, lse = c.cuda().attend()
+    assert torch.isnan(o.float()).all() and torch.isfinite(lse).all() and fb.fp_get_device_status() == 0
+    c.pool["v"].view(torch.uint8).flatten(0, 1)[c.flat(0, np.array([3]))] = 0
+    o, lse = c.cuda().attend()
+    check_tree(c, o, lse)
