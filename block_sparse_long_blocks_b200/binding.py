@@ -341,6 +341,9 @@ def _native():
         loader = importlib.machinery.ExtensionFileLoader("_calls", _CALLS_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
         loader.exec_module(module)
+        if module.torch_version != torch.__version__:
+            raise RuntimeError(f"{_CALLS_PATH} was built for torch {module.torch_version}, this is {torch.__version__}: "
+                               "build it again with `python -m block_sparse_long_blocks_b200.build`")
         module.bind(LIB_PATH)
         _calls = module
     return _calls

@@ -7,7 +7,7 @@ library with the CUDA runtime linked statically, so the library depends only on
 the driver. The build is skipped when the library is newer than every source.
 
 ``build_calls()`` compiles ``native/calls.cpp``, the per-step calls' CPython module,
-against the installed torch into ``_calls.so``.
+against the installed torch into ``_calls.so``; ``build()`` of the library includes it.
 
 ``build_variant(name, defines)`` builds the same sources with extra
 preprocessor definitions into ``libflashprefill_<name>.so`` (objects in
@@ -85,6 +85,8 @@ def build_variant(name: str, defines=None, force: bool = False, quiet: bool = Tr
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False, lib: str = LIB,
           build_dir: str = BUILD, defines=None) -> str:
+    if lib == LIB:  # (what the binding loads beside it)
+        build_calls(force=force)
     if not force and up_to_date(lib):
         return lib
     os.makedirs(build_dir, exist_ok=True)
@@ -107,12 +109,25 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False,
 
 CALLS_SRC = os.path.join(PKG, "native", "calls.cpp")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_STAMP = os.path.join(BUILD, "calls.torch")  # the torch and Python that CALLS was built for
+
+
+def calls_target() -> str:
+    import torch
+    return f"{torch.__version__} {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sys.version}"
+
+
+def calls_up_to_date() -> bool:
+    newest = max(os.path.getmtime(p) for p in (CALLS_SRC, os.path.join(INCLUDE, "flashprefill.h"), os.path.abspath(__file__)))
+    if not os.path.exists(CALLS) or os.path.getmtime(CALLS) < newest or not os.path.exists(CALLS_STAMP):
+        return False
+    with open(CALLS_STAMP) as f:
+        return f.read() == calls_target()
 
 
 def build_calls(force: bool = False) -> str:
     """The CPython module of the per-step calls (host code only)."""
-    newest = max(os.path.getmtime(p) for p in (CALLS_SRC, os.path.join(INCLUDE, "flashprefill.h"), os.path.abspath(__file__)))
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+    if not force and calls_up_to_date():
         return CALLS
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
@@ -122,11 +137,15 @@ def build_calls(force: bool = False) -> str:
     tmp = CALLS + ".tmp"
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", CALLS_SRC,
            "-o", tmp, *[f"-I{d}" for d in dirs], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DFP_TORCH_VERSION="{torch.__version__}"',
            f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}{r.stderr}")
     os.replace(tmp, CALLS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(calls_target())
     return CALLS
 
 
@@ -136,7 +155,7 @@ def main():
     ap.add_argument("--verbose-ptxas", action="store_true")
     a = ap.parse_args()
     print(build(force=a.force, verbose_ptxas=a.verbose_ptxas))
-    print(build_calls(force=a.force))
+    print(CALLS)
 
 
 if __name__ == "__main__":

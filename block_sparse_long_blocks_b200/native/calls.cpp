@@ -239,4 +239,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+// torch_version: the torch whose headers (tensor layout, inline accessors) this file was compiled with.
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", FP_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -1,6 +1,7 @@
 """The paged-cache entry points without a GPU: what they refuse before any CUDA call, the
 binding's own checks, and the float64 reference the GPU tests use."""
 import ctypes
+import subprocess
 
 import numpy as np
 import pytest
@@ -193,6 +194,38 @@ def test_native_calls_check_before_any_cuda_call(lib):
         fb.fp_cache_write(cache, [0, 1, 3], k, k)
     with pytest.raises(TypeError):
         fb.fp_cache_write(cache, c.cu, k, None)
+
+
+def test_build_includes_the_per_step_calls(monkeypatch, tmp_path):
+    """`build()` brings the module that the binding loads beside the library, and again for another torch."""
+    made = []
+
+    def compiler(cmd, **kw):
+        made.append(cmd[cmd.index("-o") + 1])
+        open(made[-1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build, "CALLS_STAMP", str(tmp_path / "stamp"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "up_to_date", lambda lib: True)  # (the library itself)
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    build.build()
+    assert made == [build.CALLS + ".tmp"]
+    build.build()
+    assert len(made) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    build.build()
+    assert len(made) == 2
+
+
+def test_calls_of_another_torch_are_refused(lib, monkeypatch):
+    monkeypatch.setattr(fb, "_calls", None)
+    fb._native()
+    monkeypatch.setattr(fb, "_calls", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    with pytest.raises(RuntimeError, match="was built for torch"):
+        fb._native()
 
 
 def test_native_tree_refuses_rows_repeated_by_a_zero_stride(lib):
