@@ -5,7 +5,7 @@
 #include <cstdint>
 #include <mutex>
 
-#include "internal.cuh"
+#include "cache.cuh"
 
 namespace fp {
 

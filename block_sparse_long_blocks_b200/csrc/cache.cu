@@ -16,7 +16,7 @@
 
 #include <type_traits>
 
-#include "internal.cuh"
+#include "cache.cuh"
 #include "packed.cuh"
 
 namespace fp {

@@ -4,7 +4,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "internal.cuh"
+#include "cache.cuh"
 
 namespace fp {
 

@@ -2,7 +2,7 @@
 #include <cstdio>
 #include <mutex>
 
-#include "internal.cuh"
+#include "cache.cuh"
 
 namespace fp {
 
@@ -50,6 +50,11 @@ bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const vo
     return false;
   }
   return true;
+}
+
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box) {
+  return encode_tiled(map, type, rank, base, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace fp

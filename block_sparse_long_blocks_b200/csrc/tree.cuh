@@ -7,7 +7,7 @@
 
 #include <atomic>
 
-#include "internal.cuh"
+#include "cache.cuh"
 #include "sm100.cuh"
 
 namespace fp {

@@ -21,3 +21,9 @@ def test_extrapolation_scales_with_the_unsampled_work():
                 visits=500, N=N, wall=3.0)
     # half the rows, half the scoring work and half the visits: twice the row work
     assert abs(bench.extrapolate(half, w, total_visits=1000) - (0.5 + 2.0 + 3.0)) < 1e-12
+
+
+def test_recorded_traffic_belongs_to_the_sources():
+    """The committed DRAM record is of the attention kernel as it stands (else the roofline has no traffic)."""
+    for dtype in ("bf16", "e4m3"):
+        assert bench.recorded_traffic("qwen30b_128k", dtype) > 0
