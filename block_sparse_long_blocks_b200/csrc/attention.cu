@@ -38,9 +38,12 @@
 #include <cstdio>
 
 #include "internal.cuh"
+#include "packed.cuh"
 #include "sm100.cuh"
 
 namespace fp {
+
+using namespace packed;
 
 namespace {
 
@@ -101,21 +104,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// ---- packed float32x2 arithmetic (one instruction for two lanes' worth of work)
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
 }
 
 // One pair of softmax weights 2^(s*sl2 - m) on MUFU.EX2, after a scale-and-subtract
