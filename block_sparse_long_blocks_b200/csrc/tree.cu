@@ -131,7 +131,8 @@ struct Cfg {
   static constexpr int SLOT = kTileBytes + (E4M3 ? 1024 : 0);  // + the tile's token scales
   static constexpr int SLOTS = 5;
   static constexpr int ROWS = 8 * NB;
-  static constexpr int QT = E4M3 ? NB : (NB + 1) / 2;    // 16-row A tiles of Q (e4m3: high and low parts)
+  static_assert(NB <= 2, "an A tile has 16 rows");
+  static constexpr int QT = E4M3 ? NB : 1;               // 16-row A tiles of Q (e4m3: high, then low parts)
   // the warps' O meet in NB rounds of D / NB columns; rows are padded so that the fragments' stores hit 32 banks
   static constexpr int RED_COLS = D / NB, RED_ROW = RED_COLS + 4;
   static constexpr int RED = kWarps * ROWS * RED_ROW * 4;
@@ -149,12 +150,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const __grid_constant__ TreeArgs a) {
   using C = Cfg<E4M3, D, NB>;
-  constexpr int BLOCKS = C::TILE / kWarps / 16;         // 16-key blocks per warp and tile,
-  constexpr int STEPS = NB == 4 || BLOCKS < 2 ? 1 : 2;  // of which so many share a softmax update
+  constexpr int STEPS = C::TILE / kWarps / 16;          // 16-key blocks per warp and tile: one softmax update
+  static_assert(STEPS <= 2 && (!E4M3 || STEPS == 2), "blocks of a warp");
   constexpr int KS = D * C::ES / 32;                    // 32-byte steps of a row
   constexpr int MT = D / 16;                            // 16-column tiles of O
   constexpr int QT = C::QT;
-  constexpr bool Q_REGS = NB <= 2;                      // Q's fragments stay in registers
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red = reinterpret_cast<float*>(ring + C::SLOTS * C::SLOT);
@@ -276,18 +276,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int n = lane & 7, hi = (lane >> 3) & 1;
     const int kk = lane < 16 ? n : 8 + (E4M3 ? n ^ 4 : n);  // K: lanes 16-31 hold tile 1
-    k_lane = smem_u32(ring) + (warp * BLOCKS * 16 + kk) * 128 + (((hi ^ kk) & 7) << 4);
+    k_lane = smem_u32(ring) + (warp * STEPS * 16 + kk) * 128 + (((hi ^ kk) & 7) << 4);
     int vk, vg;                                             // V: key, and granule (16 bytes) within a d tile's
     if (E4M3) {
       const int i = lane & 15, pair = 2 * (i >> 2) + (i & 1);
       vk = (i & 2) ? 8 + (pair ^ 4) : pair;
-      vg = STEPS == 1 ? lane >> 4 : 0;                      // lanes 16-31: the next d tile, or the next block's keys
-      if (STEPS == 2) vk += lane & 16;
+      vg = 0;
+      vk += lane & 16;                                      // lanes 16-31: the next block's keys
     } else {
       vk = ((lane >> 4) << 3) + n;
       vg = hi;
     }
-    v_lane = smem_u32(ring) + (warp * BLOCKS * 16 + vk) * 128 + (((vg ^ vk) & 7) << 4);
+    v_lane = smem_u32(ring) + (warp * STEPS * 16 + vk) * 128 + (((vg ^ vk) & 7) << 4);
     const int qr = lane & 15, qh = lane >> 4;
     q_lane = smem_u32(q_smem) + qr * 128 + (((qh ^ qr) & 7) << 4);
   }
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // times 2^(7 - floor(log2 max)): the largest lies in [2^7, 2^8); rows of zeros or below 2^-100 take the limits
       const int e = mx == 0.f ? 7 : max((int)((__float_as_uint(mx) >> 23) & 255u) - 127, -100);
       const float up = mx < INFINITY ? __uint_as_float((uint32_t)(7 - e + 127) << 23) : __uint_as_float(0x7fc00000u);
-      const int hi_row = NB == 1 ? row : (row >> 4) * 32 + (row & 15), lo_row = hi_row + (NB == 1 ? 8 : 16);
+      const int hi_row = row, lo_row = row + C::ROWS;
 #pragma unroll
       for (int i = 0; i < EL / 4; ++i) {
         float v[4] = {__uint_as_float(w[2 * i] << 16) * up, __uint_as_float(w[2 * i] & 0xffff0000u) * up,
@@ -365,13 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     consumers_sync();
-    uint32_t qf[Q_REGS ? QT : 1][Q_REGS ? KS : 1][4];
-    if constexpr (Q_REGS) {
+    uint32_t qf[QT][KS][4];
 #pragma unroll
-      for (int qt = 0; qt < QT; ++qt)
+    for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) load_q(qf[qt][ks], qt, ks);
-    }
+      for (int ks = 0; ks < KS; ++ks) load_q(qf[qt][ks], qt, ks);
     // this thread's rows of S: gr + 8 b
     float sl2[NB];
     int tok[NB];
@@ -428,15 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int qt = 0; qt < QT; ++qt) {
-            uint32_t tmp[4];
-            if constexpr (!Q_REGS) load_q(tmp, qt, ks);
-            const uint32_t(&qa)[4] = Q_REGS ? qf[Q_REGS ? qt : 0][Q_REGS ? ks : 0] : tmp;
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
-                if constexpr (E4M3) mma16832(acc[st][nt][qt], qa, kb[st][2 * nt], kb[st][2 * nt + 1]);
-                else mma16816<false>(acc[st][nt][qt], qa, kb[st][2 * nt], kb[st][2 * nt + 1]);
+                if constexpr (E4M3) mma16832(acc[st][nt][qt], qf[qt][ks], kb[st][2 * nt], kb[st][2 * nt + 1]);
+                else mma16816<false>(acc[st][nt][qt], qf[qt][ks], kb[st][2 * nt], kb[st][2 * nt + 1]);
               }
           }
         }
@@ -448,11 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                if constexpr (!E4M3) s[st][b][nt][e] = acc[st][nt][b >> 1][(b & 1) * 2 + e];
+                if constexpr (!E4M3) s[st][b][nt][e] = acc[st][nt][0][b * 2 + e];
                 else if constexpr (NB == 1) s[st][b][nt][e] = fmaf(acc[st][nt][0][2 + e], 0x1p-5f, acc[st][nt][0][e]);
-                else
-                  s[st][b][nt][e] = fmaf(acc[st][nt][(b & ~1) + 1][(b & 1) * 2 + e], 0x1p-5f,
-                                         acc[st][nt][b & ~1][(b & 1) * 2 + e]);
+                else s[st][b][nt][e] = fmaf(acc[st][nt][QT - 1][b * 2 + e], 0x1p-5f, acc[st][nt][0][b * 2 + e]);
               }
       }
       // V rows that enter the product: masks of this thread's keys (e4m3: four bytes; bf16: two halves of two words),
@@ -629,18 +622,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       } else {
 #pragma unroll
-        for (int mt = 0; mt < MT; mt += STEPS == 1 ? 2 : 1) {
+        for (int mt = 0; mt < MT; ++mt) {
           uint32_t w[4];
           ldsm2_t8(w, va ^ (mt << 4));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {  // the load's halves: another d tile, or another block of keys
-            const int st = STEPS == 1 ? 0 : i, tile = STEPS == 1 ? mt + i : mt;
-            clean(w[2 * i], st, 0);
-            clean(w[2 * i + 1], st, 0);
-            const uint32_t f[4] = {widen_lo(w[2 * i]), widen_lo(w[2 * i + 1]), widen_hi(w[2 * i]),
-                                   widen_hi(w[2 * i + 1])};
+          for (int st = 0; st < 2; ++st) {  // the load's halves: a block of keys each
+            clean(w[2 * st], st, 0);
+            clean(w[2 * st + 1], st, 0);
+            const uint32_t f[4] = {widen_lo(w[2 * st]), widen_lo(w[2 * st + 1]), widen_hi(w[2 * st]),
+                                   widen_hi(w[2 * st + 1])};
 #pragma unroll
-            for (int b = 0; b < NB; ++b) mma16816<true>(o[tile][b], f, pf[st][b][0], pf[st][b][1]);
+            for (int b = 0; b < NB; ++b) mma16816<true>(o[mt][b], f, pf[st][b][0], pf[st][b][1]);
           }
         }
       }
@@ -657,15 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = mbar_wait<true>(full + kslot, kphase, abort_flag, g.status, FP_DEV_TIMEOUT);
       const float* ksc = reinterpret_cast<const float*>(ring + kslot * C::SLOT + kTileBytes);
       const float* vsc = reinterpret_cast<const float*>(ring + vslot * C::SLOT + kTileBytes);
-#pragma unroll 1
-      for (int st = 0; st < BLOCKS; st += STEPS) {
-        const int k0 = (warp * BLOCKS + st) * 16;
-        const uint32_t ka = k_lane + kslot * C::SLOT + st * (16 * 128), va = v_lane + vslot * C::SLOT + st * (16 * 128);
-        if (t * C::TILE + k0 + STEPS * 16 > sg.base)
-          update(std::true_type(), t * C::TILE + k0, k0, ka, va, ksc, vsc, full + vslot, vphase);
-        else
-          update(std::false_type(), t * C::TILE + k0, k0, ka, va, ksc, vsc, full + vslot, vphase);
-      }
+      const int k0 = warp * STEPS * 16;
+      const uint32_t ka = k_lane + kslot * C::SLOT, va = v_lane + vslot * C::SLOT;
+      if (t * C::TILE + k0 + STEPS * 16 > sg.base)
+        update(std::true_type(), t * C::TILE + k0, k0, ka, va, ksc, vsc, full + vslot, vphase);
+      else
+        update(std::false_type(), t * C::TILE + k0, k0, ka, va, ksc, vsc, full + vslot, vphase);
       __syncwarp();
       if (ok && lane == 0) {
         mbar_arrive(empty + kslot);
