@@ -363,7 +363,9 @@ class Cache:
     (cached tokens of every request, the new tokens of the call included; read
     on the device, so a program updates it in place). e4m3 pools take float32
     scales: [hkv] (one per KV head) or [pages, hkv, page] (one per token and
-    head, written by ``fp_cache_write``). Holds the tensors; copies nothing."""
+    head, written by ``fp_cache_write``). Holds the tensors; copies nothing.
+    Allocate the pools with ``torch.zeros``: the prefill needs finite V behind a
+    request's last token."""
 
     def __init__(self, k_pool, v_pool, page_table, kv_lens, k_scale=None, v_scale=None):
         if not (k_pool.dim() == 4 and k_pool.shape == v_pool.shape and k_pool.dtype == v_pool.dtype

@@ -38,7 +38,8 @@
 // f16 instruction's for twice the keys, and needs no widening; its sums were
 // measured exact to 2^-22 of sum |q k|), with q * 2^e (e per row such that max |q|
 // lies in [2^7, 2^8)) as hi + 2^-5 lo, two e4m3 values whose sum is q exactly for
-// every element within 2^-15 of the largest; up to 8 rows both fill one M tile.
+// every element within 2^-14 of the largest, and to 2^-22 of it for others; up to
+// 8 rows both fill one M tile.
 // V is widened exactly to f16; p carries a factor 2^kShift into f16's normal
 // range. Token scales of V multiply p, and f16 holds the product p v_scale
 // relative to the row's own largest one so far (its logarithm's reference is kept

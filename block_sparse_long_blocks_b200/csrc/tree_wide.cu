@@ -23,9 +23,9 @@
 // Operands: bf16 caches multiply bf16, with P rounded to bf16 (as hi + lo, 191
 // us, otherwise 165). e4m3 caches: S on the e4m3 path with q * 2^e (e per row
 // such that max |q| lies in [2^7, 2^8)) as the sum hi + lo of two e4m3 values,
-// exact for elements within 2^-10 of the row's largest, others to 2^-18 of it;
-// the two products take the time of one on 16-bit operands, and K is multiplied
-// as it was loaded. V is widened exactly to f16 by the converters, P goes to f16.
+// exact for elements within 2^-9 of the row's largest, others to 2^-17 of it (both
+// products go to the same accumulators, which leaves no factor for lo); they take
+// the time of one on 16-bit operands, and K is multiplied as it was loaded. V is widened exactly to f16 by the converters, P goes to f16.
 // The converters also pass the V tiles on in order, and make those that hold new
 // tokens or end behind the last one safe to multiply: rows behind the last token
 // become zeros, and so do infinities and NaN of new tokens, which only some rows

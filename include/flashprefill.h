@@ -43,6 +43,12 @@
  * - Paged KV (page_table != NULL, requires cu_seqlens): K/V live in pools
  *   [num_pages, page_size, Hkv, d]; token t of request r is slot t % page_size
  *   of pool page page_table[r * max_pages_per_req + t / page_size].
+ * - V behind a request's end: the prefill attention multiplies the rest of a
+ *   request's last block, with weights of zero, by the V rows that follow it (the
+ *   slots behind its last token; without a page table the next request's rows).
+ *   They have to be finite: infinity or NaN there makes rows of that block NaN.
+ *   A pool that is zeroed once, when it is allocated, meets this whatever tokens
+ *   its pages held before. (The decoding calls below do not need it.)
  * - Chunked prefill with a cached prefix (kv_lens != NULL; needs cu_seqlens
  *   and page_table): request r has kv_lens[r] tokens in the paged KV cache and
  *   its queries are its LAST q_len_r = cu[r+1] - cu[r] tokens (positions
@@ -261,7 +267,8 @@ size_t fp_static_scratch_bytes(void);
  *   cu[r] .. cu[r+1]-1 of the packed tensors, which have total_tokens rows.
  *   They are the request's LAST n_r positions, kv_lens[r] - n_r ..
  *   kv_lens[r] - 1 (kv_lens counts them; as in chunked prefill). n_r may be 0.
- *   Packed rows outside every request are neither read nor written.
+ *   Packed rows outside every request are not written, and what they hold does
+ *   not matter (fp_cache_write may load them).
  * - Checked on the device: a request whose cu_tokens or kv_lens do not fit
  *   (n_r < 0, cu[r+1] > total_tokens, n_r > kv_lens[r], kv_lens[r] >
  *   max_pages_per_req * page_size) sets FP_DEV_BAD_SEQLENS and is skipped; a
@@ -295,8 +302,8 @@ typedef struct {
  * hkv * head_dim, so that slices of a fused projection need no copy) into the
  * cache. FP_E4M3: code = x / scale, clamped to +-448 and rounded to nearest
  * even (NaN stays NaN); with FP_SCALE_TOKEN the scale of a token and head is
- * the float32 max |x| / 448 over its head_dim values (0 for a zero row, whose
- * codes are 0), and is stored beside the codes. FP_SCALE_HEAD reads the given
+ * the float32 max |x| / 448 over its head_dim values that are not NaN (0 for a
+ * row of zeros, whose codes are zeros), and is stored beside the codes. FP_SCALE_HEAD reads the given
  * scales; a head scale of 0 is taken as 1.
  */
 fp_status_t fp_cache_write(const fp_cache_t* c, const int32_t* cu_tokens, int total_tokens, const void* k,
@@ -355,10 +362,17 @@ size_t fp_tree_workspace_size(const fp_cache_t* c, const fp_tree_t* t);
  * [hq, total_tokens] (natural log). A row that sees nothing gets O = 0 and
  * lse = -inf. Cached values at positions a row does not see, and slots at or
  * behind kv_lens[r], do not reach its result, whatever they hold (NaN and
- * infinities too). Scores, softmax sums and O are float32; the weights enter
- * O += P V as f16 (e4m3 caches), or (bf16 caches) as bf16 pairs hi + lo, or, of
- * requests with more than 16 rows (max_tokens * hq / hkv), as bf16, divided by
- * the sum of the rounded weights.
+ * infinities too). An infinity of V that a row sees gives that infinity, or NaN
+ * where its weight is below 2^-126 of the row's largest.
+ * Scores, softmax sums and O are float32. By rows, max_tokens * hq / hkv:
+ *                               up to 16              more
+ *   weights in O += P V, bf16   bf16 pairs hi + lo    bf16, divided by their sum
+ *   ... e4m3                    f16                   f16
+ *   q with e4m3 caches: elements within 2^-14 (more than 16 rows: 2^-9) of their
+ *   row's largest are exact, others rounded to 2^-22 (2^-17) of it
+ * 17 to 32 rows are treated as up to 16 where the page table has room for 1 MB of
+ * a KV head's K and V at most (max_pages_per_req * page_size tokens), so there
+ * the last bits follow the table's width.
  * The keys of all requests are divided evenly over the SMs; partial results
  * are combined in a fixed order, so equal calls give equal bits.
  * A request with n_r > max_tokens sets FP_DEV_BAD_SEQLENS and is skipped.

@@ -185,3 +185,35 @@ def test_nan_of_a_value_reaches_a_row_that_hardly_weighs_it(G, n, kv, fmt):
     c.pool["v"].view(torch.uint8).flatten(0, 1)[c.flat(0, np.array([3]))] = 0
     o, lse = c.cuda().attend()
     check_tree(c, o, lse)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3_head", "e4m3_token"])
+@pytest.mark.parametrize("outlier", [300.0, -1e4])
+@pytest.mark.parametrize("G,n", KERNELS)
+def test_a_query_with_an_outlier_element(G, n, outlier, fmt):
+    """One element of a query is far above the others; K is small in its channel, as a model's would be.
+
+    q of e4m3 caches is the sum of two e4m3 values, off by at most eps = 2^-22 (more than 16 rows: 2^-17) of the row's
+    largest element, which puts an exponent off by at most B = eps max|q| scale sum|k|, a weight by e^B - 1 relative, lse by
+    as much and O, a quotient, by twice that of W."""
+    c = Case([n + 200], [n], hkv=2, G=G, fmt=fmt, seed=n).trees()
+    shrink = 2.0 ** -6 if abs(outlier) < 1000 else 2.0 ** -11
+    k = c.pool["k"].float()
+    k[..., 7] *= shrink
+    c.pool["k"] = k.to(c.pool["k"].dtype)
+    c.q[0, 1, 7] = c.q[n - 1, c.hq - 1, 7] = outlier
+    o, lse = c.cuda().attend()
+    O, L, W, A = pc.tree_attention(c.oracle(), c.cu.numpy(), c.q.double().numpy(), c.see, 1 / np.sqrt(c.d))
+    eps = 0.0 if fmt == "bf16" else 2.0 ** -22 if n * G <= 16 else 2.0 ** -17
+    flat = c.flat(0, np.arange(c.kv[0])).numpy()
+    K = np.repeat(np.abs(pc.tokens(c.oracle(), "k", flat)).sum(-1).max(0), G)  # [hq]: the largest sum|k|
+    B = eps * c.q.double().abs().amax(-1).numpy() * K / np.sqrt(c.d)
+    delta = 2 * (c.d + 8) * 2.0 ** -23 * A + 2.0 ** -21 + (c.kv[0] / 16 + 16) * 2.0 ** -23 + np.expm1(B)
+    p_round = 2.0 ** -11 if fmt != "bf16" else 2.0 ** -7 if n * G > 16 else 2.0 ** -16
+    # f16 below its normal range: 2^-33 of the row's largest product a key (see check_rows), V's rows being within 2^6
+    tol = 2.0 ** -8 * np.abs(O) + (2 * delta + 2.0 ** -15 + p_round)[..., None] * W * 1.01 \
+        + c.kv[0] * 2.0 ** -33 * 64 * W.max(-1)[..., None]
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(o - O) <= tol).all(), f"O off by {(np.abs(o - O) / tol).max():.2f} of its bound"
+    assert (np.abs(lse - L) <= delta.T + 2.0 ** -22 * (np.abs(L) + 4)).all()
+    assert fb.fp_get_device_status() == 0
