@@ -456,7 +456,7 @@ MoveArgs move_args(const CacheGeometry& g, const int32_t* starts, const void* k,
   a.v_stride = v_stride * 2;
   a.vecs = g.Hkv * g.d / kVec;
   a.vecs_inv = (uint32_t)(((1ull << 32) + a.vecs - 1) / a.vecs);
-  const int ctas = 148 * ctas_per_sm, per = (int)(((long long)g.total_tokens + ctas - 1) / ctas);
+  const int ctas = sm_count() * ctas_per_sm, per = (int)(((long long)g.total_tokens + ctas - 1) / ctas);
   const int most = kVectorsPerCta / a.vecs < kMaxTokensPerCta ? kVectorsPerCta / a.vecs : kMaxTokensPerCta;
   a.tokens = per > most ? (most > 1 ? most : 1) : per;
   return a;

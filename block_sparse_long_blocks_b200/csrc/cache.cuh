@@ -8,6 +8,9 @@ namespace fp {
 // The status word (FP_DEV_*) of the current device; nullptr on a runtime error.
 unsigned* status_ptr();
 
+// SMs of the current device (at most 256: the combining kernel's registers).
+int sm_count();
+
 // encode_tiled with another L2 promotion than 256 bytes.
 bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
                   const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapL2promotion promotion);

@@ -1,5 +1,6 @@
 // C ABI of the paged cache and the attention over it: argument validation and
 // launches on the caller's stream.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -100,6 +101,18 @@ fp_status_t validate_tree(const fp_cache_t* c, const fp_tree_t* t) {
 }
 
 }  // namespace
+
+int sm_count() {
+  static std::atomic<int> counts[64];  // per device, 0: not asked yet
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  n = n < 256 ? n : 256;
+  if (dev < 64) counts[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace fp
 
 using namespace fp;

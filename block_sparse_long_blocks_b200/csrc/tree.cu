@@ -909,17 +909,6 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-int sm_count() {
-  static std::atomic<int> counts[64];  // per device, 0: not asked yet
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (dev < 64 && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
-  n = n < 256 ? n : 256;
-  if (dev < 64) counts[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 // Rows per unit: the kernel here holds 8 or 16, the one for many rows (tree_wide.cu) one or two M-tiles of 128. 17 to
 // 32 rows are two units here where the page table has room for 1 MB of K and V per KV head at most: a segment of many
 // rows takes 25000 clocks beside its tiles, here 4500 (16 requests, 4 KV heads, 32 rows: 256 keys 15.1 -> 11.2 us,
@@ -1010,7 +999,7 @@ fp_status_t launch_tree(const CacheGeometry& g, const fp_tree_t& t, const void* 
   a.lse = lse;
   const double scale = t.softmax_scale > 0.f ? (double)t.softmax_scale : 1.0 / std::sqrt((double)g.d);
   a.scale_log2 = (float)(scale * 1.4426950408889634);
-  a.grid = sm_count();  // (at most 256: the combining kernel's registers)
+  a.grid = sm_count();
   a.tile = a.rows <= 16 ? kTileBytes / (g.d * (g.e4m3 ? 1 : 2)) : 128;
   a.lead = a.rows <= 16 ? kNarrowLead : kWideLead;
   a.min_share = a.rows <= 16 ? 1 : 2;
