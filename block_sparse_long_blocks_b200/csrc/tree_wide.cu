@@ -436,8 +436,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::THREADS, 1)
             }
             at = make_float2(sc.x * kScaleDown, sc.y * kScaleDown);
             reinterpret_cast<float2*>(s_vlog + tn % kLogs * kKeys)[ct] = make_float2(scale_log2(sc.x), scale_log2(sc.y));
-            // (scales are not negative: they compare as integers)
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(sc.x), __float_as_uint(sc.y)));
+            // (scales are not negative: without the sign of a -0 they compare as integers)
+            const uint32_t top =
+                __reduce_max_sync(0xffffffffu, max(__float_as_uint(fabsf(sc.x)), __float_as_uint(fabsf(sc.y))));
             if (lane == 0) s_vmax[tn % kLogs * 2 + (cw & 1)] = top;
             mbar_arrive(log_full + tn % kLogs);
           }

@@ -112,6 +112,21 @@ def test_token_scales_of_any_size_and_zero(G, n, factor):
 
 
 @pytest.mark.parametrize("G,n", KERNELS)
+def test_a_scale_of_minus_zero_is_zero(G, n):
+    """Bits with scales of -0.0 are those with 0.0, whatever else the tile holds."""
+    outs = []
+    for zero in (0.0, -0.0):
+        c = Case([n + 400, n], [n, n], hkv=2, G=G, fmt="e4m3_token", seed=n).trees()
+        big = c.flat(0, np.arange(150, 390, 5))
+        c.scale["v"][big // c.page, :, big % c.page] *= 2.0 ** 30  # (references rise there)
+        at = torch.cat([c.flat(0, np.arange(5, 400, 17)), c.new_slots(1)[[1]]])
+        c.scale["v"][at // c.page, :, at % c.page] = zero
+        outs.append(c.cuda().attend())
+        check_rows(c, *outs[-1])
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("G,n", KERNELS)
 def test_uneven_scales_over_keys_split_between_ctas(G, n):
     """Keys over many CTAs, their scales spread over 2^60: the partial rows' references differ as much."""
     c = Case([6000, 17 + n, 2500], [n, 1, n], hkv=2, G=G, page=32, fmt="e4m3_token", seed=G + n).trees()
