@@ -8,9 +8,11 @@
 // in flight. The chain cu_tokens -> kv_lens -> page table that leads to a row's
 // slot is walked once per CTA (by one warp, for all of the CTA's tokens) while
 // the first vectors are already on their way.
-// Measured: prompts of 4K-64K tokens, 8 heads, into an e4m3 cache 214 us (5.8
-// TB/s), out of one 197 us (6.4 TB/s); a chunk of 32K tokens of 4 heads with
-// token scales 24 us (4.2 TB/s); one token of eight requests 2.3 us.
+// Measured on the device, calls back to back: prompts of 4K-64K tokens, 8 heads,
+// into an e4m3 cache 216 us (5.8 TB/s), out of one 198 us (6.4 TB/s), bf16 261 and
+// 256 us (6.4 and 6.5 TB/s); a chunk of 32K tokens of 4 heads with token scales
+// 24.4 us (4.2 TB/s); one token of eight requests 2.1 us. As calls between whose
+// inputs the caches turn cold: 242, 201, 27 and 3.8 us (5.2, 6.3, 3.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

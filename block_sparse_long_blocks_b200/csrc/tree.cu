@@ -18,10 +18,10 @@
 // O = sum_i 2^(lse_i - lse) O_i.
 // This file: units of 8 or 16 rows, single tokens and small trees. More rows go
 // to tree_wide.cu, where tcgen05 multiplies M-tiles of 128.
-// Measured: one token each of eight requests of 4K-64K (bf16, 8 KV heads of 4
-// query heads) 183 us, 6.5 TB/s with everything; one token of 128K (e4m3 with
-// token scales, 4 KV heads of 8) 36 us, of which 20 us stream at 6.8 TB/s; one
-// token of 2K 9 us, two launches.
+// Measured, calls whose inputs change: one token each of eight requests of 4K-64K
+// (bf16, 8 KV heads of 4 query heads) 177 to 183 us, 6.5 to 6.7 TB/s with everything;
+// one token of 128K (e4m3 with token scales, 4 KV heads of 8) 36 us, of which 20 us
+// stream at 6.8 TB/s; one token of 2K 10 us, two launches (8.8 us on the device).
 //
 // A CTA: warp 8 issues TMA copies of K and V tiles (4-D boxes per page, 128-byte
 // swizzle, and the tile's token scales) into a ring of five 32 KB slots; warps
